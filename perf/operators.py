@@ -1,0 +1,556 @@
+"""Measured cases of four cache operators, with their plain forms.
+
+  write    kvq_append_chunk: a ragged chunk of new tokens into a cache that may already hold some
+           (quantized groups, values and the bf16 window), read back by kvq_read_tokens
+  read     kvq_read_tokens: a token range of every sequence as bf16 keys and values
+  chunk    kvq_chunk_attention: a ragged chunk of new tokens attends to the packed cache and,
+           causally, to itself; with a sliding window and first tokens that stay visible, or without
+  window   kvq_decode_attention_window: one query per sequence over the last `window` cached tokens
+           and the first `sinks`
+
+The cache formats are those of include/kvq.h: 2 and 4 (INT2 / INT4, per-channel key groups of `group`
+tokens, per-token values, the last `residual` tokens or more in bf16), 6 (each group at 4 or 2 bits by
+its tokens' classes), 8 (FP8-E4M3, a static scale per head), 16 (INT8 per token).
+"""
+import math
+
+import torch
+
+own = False
+
+D = 128
+SCALE = 1.0 / math.sqrt(D)
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+
+def _spread(n, batch, least):
+    """Lengths of a ragged batch: the first is n, the others fixed fractions of it, most of them odd."""
+    out = [n]
+    for b in range(1, batch):
+        f = (0.6180339887 * b + 0.21) % 1.0
+        out.append(max(least, int(least + f * (n - least))))
+    return out
+
+
+def _lens(case):
+    """(cached tokens, new tokens) of every sequence."""
+    B = case["batch"]
+    held = _spread(case["len"], B, max(1, case["len"] // 16)) if case["ragged"] else [case["len"]] * B
+    new = case.get("new", 0)
+    new = _spread(new, B, min(1, new)) if case["ragged"] else [new] * B
+    return held, new
+
+
+def _quantized(case, n):
+    """Tokens of a sequence of n that are quantized; the others are in the bf16 window."""
+    if case["fmt"] in (8, 16):
+        return n
+    return case["group"] * (max(n - case["residual"], 0) // case["group"])
+
+
+def _case(name, op, fmt, batch, hq, hkv, length, new=0, ragged=False, group=32, residual=128, paged=False, window=0,
+          sinks=0):
+    return {"name": name, "op": op, "fmt": fmt, "batch": batch, "hq": hq, "hkv": hkv, "len": length, "new": new,
+            "ragged": ragged, "group": group, "residual": residual, "paged": paged, "window": window, "sinks": sinks}
+
+
+def listed():
+    return [
+        # a few drafted tokens of a small batch join an INT8 cache (speculative decoding): a few microseconds
+        _case("write int8 few", "write", 16, 4, 32, 8, 61, 5, ragged=True),
+        # chunked prefill of an 8B-model layer: the second piece of eight prompts
+        _case("write int4 pieces", "write", 4, 8, 32, 8, 1000, 1048),
+        # a ragged batch in 16-token pages
+        _case("write int2 paged ragged", "write", 2, 16, 32, 8, 777, 1301, ragged=True, group=16, residual=16, paged=True),
+        # a streaming start state read back whole (the cache of 16 sequences handed to another engine)
+        _case("read fp8 streaming", "read", 8, 16, 32, 8, 4096),
+        # one layer of a 70B model's 131072-token context read back
+        _case("read int2 131072", "read", 2, 1, 64, 8, 131072),
+        # verification of 6 drafted tokens over an 8B layer's cache: few rows, long cache
+        _case("chunk int4 verify", "chunk", 4, 8, 32, 8, 8192, 6),
+        # mixed traffic: ragged chunks over a paged INT4 cache
+        _case("chunk int4 paged ragged", "chunk", 4, 12, 32, 8, 6000, 515, ragged=True, group=16, residual=16, paged=True),
+        # a large prefill piece at the end of a long context, 8B layer
+        _case("chunk int4 prefill", "chunk", 4, 1, 32, 8, 32768, 2048),
+        # a windowed layer with sinks over a long 8-bit cache
+        _case("chunk fp8 window", "chunk", 8, 2, 64, 8, 40001, 1024, window=4096, sinks=4),
+        # the same at 2 bits, 70B heads, full attention
+        _case("chunk int2 70b", "chunk", 2, 1, 64, 8, 65536, 1000),
+        # decode of an 8B layer with a window of 1024 and four sinks
+        _case("window int4 8b", "window", 4, 8, 32, 8, 8192, window=1024, sinks=4),
+        # decode of a long 70B context, half of it visible
+        _case("window int8 131072", "window", 16, 2, 64, 8, 131072, window=65000, sinks=128),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "read", "chunk", "chunk", "window"])
+    fmt = rng.choice([2, 4, 6, 8, 16])
+    paged = fmt in (2, 4) and rng.random() < 0.4
+    group = 16 if paged else rng.choice([32, 64, 128]) if fmt == 6 else rng.choice([16, 32, 64, 128])
+    residual = rng.choice([0, 16, 32, 100, 128])
+    hkv = rng.choice([1, 2, 4, 8])
+    hq = hkv * rng.choice([1, 2, 3, 4, 5, 6, 7, 8])
+    batch = _log(rng, 1, 24)
+    new = 0
+    window = sinks = 0
+    if op == "read":
+        length = _log(rng, 1, min(131072, 500000 // batch))
+    elif op == "window":
+        length = _log(rng, 1, min(131072, 1500000 // batch))
+        window, sinks = _log(rng, 1, max(1, length)), rng.choice([0, 1, 4, 130])
+    elif op == "write":
+        length, new = _log(rng, 1, 40000 // batch), _log(rng, 1, 40000 // batch)
+    else:
+        new = _log(rng, 1, 1500)
+        length = _log(rng, 1, max(2, min(60000, 40000000 // (new * batch))))
+        if rng.random() < 0.5:
+            window, sinks = _log(rng, 1, length + new), rng.choice([0, 1, 4, 130])
+    c = _case("", op, fmt, batch, hq, hkv, length, new, rng.random() < 0.6, group, residual, paged, window, sinks)
+    del c["name"]
+    return c
+
+
+def _visible(case, n, m):
+    """Keys visible to each row of a chunk of m tokens after n cached ones, summed; and the distinct cached tokens."""
+    w, s = case["window"], case["sinks"]
+    if case["op"] == "window":
+        got = n if w == 0 else min(n, w + min(s, max(n - w, 0)))
+        return got, got
+    if w == 0:
+        return n * m + m * (m + 1) // 2, n
+    pairs = sum(min(p + 1, w) + min(s, max(p + 1 - w, 0)) for p in range(n, n + m))
+    lo = max(0, n - w + 1)
+    return pairs, (n - lo) + min(s, lo)
+
+
+def work(case):
+    fmt, hq, hkv = case["fmt"], case["hq"], case["hkv"]
+    row = D if fmt in (8, 16) else D * {2: 2, 4: 4, 6: 3}[fmt] // 8       # a row's codes (6: between 2 and 4 bits)
+    # a quantized token of one head: both rows, the value's (scale, zero) and its share of the key group's
+    token = 2 * row + {8: 0, 16: 8}.get(fmt, 4 + 4 * D / case["group"])
+    held, new = _lens(case)
+    nbytes = flops = 0
+    for n, m in zip(held, new):
+        if case["op"] in ("write", "read"):
+            t = n + m
+            q = _quantized(case, t)
+            kept = q * token + (t - q) * 4 * D
+            nbytes += hkv * (kept + t * 4 * D)                            # packed read, bf16 written
+            nbytes += hkv * (t * 4 * D + kept) if case["op"] == "write" else 0
+            flops += hkv * t * 2 * D * (4 if case["op"] == "write" else 2)
+            continue
+        pairs, seen = _visible(case, n, m)
+        q = _quantized(case, n)
+        raw = min(n - q, seen)
+        nbytes += hkv * ((seen - raw) * token + raw * 4 * D)
+        rows = m if case["op"] == "chunk" else 1
+        nbytes += m * hkv * 4 * D + rows * hq * D * (4 if case["op"] == "chunk" else 6)
+        flops += 4 * D * hq * pairs
+    return {"bytes": int(nbytes), "flops": int(flops)}
+
+
+# ---------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------
+
+def _inputs(case, seed):
+    """bf16 keys, values and queries and the token classes, from the seed. Keys carry a few channels of large values
+    and values a few heavy tokens, as in trained models; queries have unit scale, so that the logits spread by about two."""
+    g = torch.Generator(device="cuda").manual_seed(1000003 * seed + 17)
+    held, new = _lens(case)
+    H, hq = case["hkv"], case["hq"]
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.float32)
+
+    hot = torch.rand(H, D, generator=g, device="cuda").argsort(1) < 4
+    factor = torch.where(hot, 8.0, 1.0)
+
+    def rows(t):
+        k = (normal(t, H, D) * factor).bfloat16()
+        heavy = torch.rand(t, 1, 1, generator=g, device="cuda") < 0.01
+        v = (normal(t, H, D) * torch.where(heavy, 5.0, 1.0)).bfloat16()
+        return k, v
+
+    x = {"held": held, "new": new}
+    x["k"], x["v"] = rows(sum(held))
+    x["k_new"], x["v_new"] = rows(sum(new))
+    x["q"] = normal(sum(new) if case["op"] == "chunk" else case["batch"], hq, D).bfloat16()
+    # classes come in stretches of one kind; three tokens in ten are kept at 4 bits
+    cls = torch.where(torch.rand(sum(held) // 48 + 2, generator=g, device="cuda") < 0.3, 4, 2).to(torch.uint8)
+    x["cls"] = cls.repeat_interleave(48)[: sum(held)].contiguous()
+    cls = torch.where(torch.rand(sum(new) // 48 + 2, generator=g, device="cuda") < 0.3, 4, 2).to(torch.uint8)
+    x["cls_new"] = cls.repeat_interleave(48)[: sum(new)].contiguous()
+    if case["fmt"] == 8:   # static scales, as a calibration leaves them: the largest magnitude over 448
+        x["amax"] = torch.stack([t.float().abs().amax((0, 2)) if t.numel() else torch.ones(H, device="cuda")
+                                 for t in (x["k"], x["v"])])
+        x["scale"] = x["amax"] / 448.0
+    pages = [-(-(n + m) // 16) for n, m in zip(held, new)]
+    x["pages"], x["pool"] = max(max(pages), 1), sum(pages) + 3
+    order = torch.rand(x["pool"], generator=g, device="cuda").argsort()[: sum(pages)].int()
+    table = torch.zeros(case["batch"], x["pages"], dtype=torch.int32, device="cuda")
+    at = 0
+    for b, p in enumerate(pages):
+        table[b, :p] = order[at:at + p]
+        at += p
+    x["table"] = table
+    return x
+
+
+def _offsets(lens):
+    return torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).int().cuda()
+
+
+def _places(case, lens):
+    """Rows of the flat [sum(lens)] tokens that are quantized, and those in the window."""
+    quantized, raw, at = [], [], 0
+    for n in lens:
+        q = _quantized(case, n)
+        quantized.append(torch.arange(at, at + q))
+        raw.append(torch.arange(at + q, at + n))
+        at += n
+    return torch.cat(quantized).cuda(), torch.cat(raw).cuda()
+
+
+# ---------------------------------------------------------------------------
+# Plain form: 32-bit elementary operations
+# ---------------------------------------------------------------------------
+
+def _encode(x, dim, levels):
+    """Codes, fp16 scale and zero of x over `dim`; every step rounded to 32 bits as include/kvq.h states it."""
+    mn, mx = x.amin(dim, keepdim=True), x.amax(dim, keepdim=True)
+    s = ((mx - mn) / levels).half()
+    z = (mn + 0.0).half()
+    inv = torch.where(s > 0, torch.ones_like(mn) / s.float(), torch.zeros_like(mn))
+    code = torch.minimum(((x - z.float()) * inv).round().clamp_min(0), torch.zeros_like(mn) + levels)
+    return code.to(torch.uint8), s, z
+
+
+def _bits(fmt):
+    return {6: 4, 16: 8}.get(fmt, fmt)
+
+
+def _pack(code, bits):
+    if bits == 8:
+        return code
+    out = code[..., 0::8 // bits].clone()
+    for i in range(1, 8 // bits):
+        out |= code[..., i::8 // bits] << (bits * i)
+    return out
+
+
+def _unpack(packed, bits):
+    if bits == 8:
+        return packed
+    return torch.stack([(packed >> (bits * i)) & (2 ** bits - 1) for i in range(8 // bits)], -1).flatten(-2)
+
+
+def _quantize(case, k, v, cls, scale):
+    """The packed form of whole groups of tokens: k, v bf16 [T, H, D], T a multiple of the group."""
+    fmt, G = case["fmt"], case["group"]
+    T, H = k.shape[:2]
+    if fmt == 8:
+        inv = torch.ones_like(scale) / scale
+        codes = [(x.float() * i[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                 for x, i in zip((k, v), inv)]
+        return {"kc": codes[0], "vc": codes[1], "scale": scale}
+    if fmt == 16:
+        kc, ks, kz = _encode(k.float(), -1, torch.tensor(255.0, device="cuda"))
+        vc, vs, vz = _encode(v.float(), -1, torch.tensor(255.0, device="cuda"))
+        return {"kc": kc, "ks": ks, "kz": kz, "vc": vc, "vs": vs, "vz": vz}
+    if fmt == 6:
+        four = (cls.view(T // G, G) == 4).any(1)
+        levels = torch.where(four, 15.0, 3.0)
+    else:
+        levels = torch.full((T // G,), 2.0 ** fmt - 1, device="cuda")
+    kc, ks, kz = _encode(k.float().view(T // G, G, H, D), 1, levels[:, None, None, None])
+    vc, vs, vz = _encode(v.float(), -1, levels.repeat_interleave(G)[:, None, None])
+    return {"kc": _pack(kc.flatten(0, 1), _bits(fmt)), "ks": ks.squeeze(1), "kz": kz.squeeze(1),
+            "vc": _pack(vc, _bits(fmt)), "vs": vs, "vz": vz}
+
+
+def _dequantize(case, p, rows):
+    """fp32 keys and values [len(rows), H, D] of the packed form's token rows."""
+    if case["fmt"] == 8:
+        return tuple(p[c][rows].view(torch.float8_e4m3fn).float() * s[:, None]
+                     for c, s in zip(("kc", "vc"), p["scale"]))
+    b = _bits(case["fmt"])
+    set_ = rows if case["fmt"] == 16 else rows // case["group"]
+    k = _unpack(p["kc"][rows], b).float() * p["ks"][set_].float() + p["kz"][set_].float()
+    v = _unpack(p["vc"][rows], b).float() * p["vs"][rows].float() + p["vz"][rows].float()
+    return k, v
+
+
+def _held(case, x, lens, k, v, cls):
+    """What the cache holds of k, v: packed groups and the window's bf16 rows."""
+    at, raw = _places(case, lens)
+    p = _quantize(case, k[at], v[at], cls[at], x.get("scale"))
+    return {"packed": p, "at": at, "raw": raw, "k_raw": k[raw], "v_raw": v[raw]}
+
+
+def _plan(case, x, h):
+    """The cached tokens that a pass needs, sequence by sequence: their positions, and where the cache has them."""
+    positions, flat, at = [], [], 0
+    for n, m in zip(x["held"], x["new"]):
+        first = n if case["op"] == "chunk" else n - 1                     # the first query's position
+        first = max(0, first - case["window"] + 1) if case["window"] else 0
+        positions.append(torch.cat([torch.arange(min(case["sinks"], first)), torch.arange(first, n)]))
+        flat.append(at + positions[-1])
+        at += n
+    flat = torch.cat(flat).cuda()
+    in_window = torch.isin(flat, h["raw"])
+    packed, raw = flat[~in_window], flat[in_window]
+    return {"positions": [p.cuda() for p in positions], "count": flat.numel(),
+            "packed": (torch.where(~in_window)[0], torch.searchsorted(h["at"], packed)),
+            "raw": (torch.where(in_window)[0], torch.searchsorted(h["raw"], raw))}
+
+
+def _rows(case, h, plan):
+    """fp32 keys and values of the plan's tokens."""
+    k = torch.empty(plan["count"], case["hkv"], D, device="cuda")
+    v = torch.empty_like(k)
+    to, rows = plan["packed"]
+    k[to], v[to] = _dequantize(case, h["packed"], rows)
+    to, rows = plan["raw"]
+    k[to], v[to] = h["k_raw"][rows].float(), h["v_raw"][rows].float()
+    return k, v
+
+
+def _attend(case, q, k, v, pos, keys):
+    """softmax(q k^T) v with its log-sum-exp: q [m, hq, D] at positions pos [m]; k, v [t, hkv, D] at positions keys [t]."""
+    w, s = case["window"], case["sinks"]
+    p = pos[:, None]
+    seen = keys <= p
+    if w:
+        seen = seen & ((keys > p - w) | (keys < s))
+    m, hq = q.shape[:2]
+    g = hq // k.shape[1]
+    qh = q.float().view(m, k.shape[1], g, D).permute(1, 2, 0, 3).reshape(k.shape[1], g * m, D) * SCALE
+    logit = (qh @ k.permute(1, 2, 0)).view(k.shape[1], g, m, -1).masked_fill(~seen, -math.inf)
+    top = logit.amax(-1, keepdim=True)
+    e = (logit - top).exp()
+    total = e.sum(-1, keepdim=True)
+    out = (e.flatten(1, 2) @ v.permute(1, 0, 2)).view(k.shape[1], g, m, D) / total
+    lse = (top + total.log()).squeeze(-1)
+    return out.permute(2, 0, 1, 3).reshape(m, hq, D), lse.permute(2, 0, 1).reshape(m, hq)
+
+
+def _run_plain(st):
+    case, x = st["case"], st["x"]
+    held, new = x["held"], x["new"]
+    if case["op"] == "write":
+        k = torch.cat([x["k"], x["k_new"]])[st["order"]]
+        v = torch.cat([x["v"], x["v_new"]])[st["order"]]
+        cls = torch.cat([x["cls"], x["cls_new"]])[st["order"]]
+        lens = [n + m for n, m in zip(held, new)]
+        h = _held(case, x, lens, k, v, cls)
+        k, v = torch.empty_like(k), torch.empty_like(v)
+        rows = torch.arange(h["at"].numel(), device="cuda")
+        for to, got in zip((k, v), _dequantize(case, h["packed"], rows)):
+            to[h["at"]] = got.bfloat16()
+        k[h["raw"]], v[h["raw"]] = h["k_raw"], h["v_raw"]
+        return {"k": k, "v": v, "seq_len": torch.tensor(lens, dtype=torch.int32).cuda(),
+                "n_quant": torch.tensor([_quantized(case, n) for n in lens], dtype=torch.int32).cuda()}
+    k, v = _rows(case, st["cache"], st["plan"])
+    if case["op"] == "read":
+        return {"k": k.bfloat16(), "v": v.bfloat16()}
+    outs, lses, at, at_new = [], [], 0, 0
+    for b, (n, m) in enumerate(zip(held, new)):
+        keys = st["plan"]["positions"][b]
+        kb, vb = k[at:at + len(keys)], v[at:at + len(keys)]
+        at += len(keys)
+        if case["op"] == "chunk":
+            part = slice(at_new, at_new + m)
+            kb, vb = torch.cat([kb, x["k_new"][part].float()]), torch.cat([vb, x["v_new"][part].float()])
+            pos = torch.arange(n, n + m, device="cuda")
+            o, s = _attend(case, x["q"][part], kb, vb, pos, torch.cat([keys, pos]))
+            at_new += m
+        else:
+            o, s = _attend(case, x["q"][b:b + 1], kb, vb, torch.full((1,), n - 1, device="cuda"), keys)
+        outs.append(o)
+        lses.append(s)
+    if case["op"] == "chunk":
+        return torch.cat(outs).bfloat16()
+    return {"out": torch.cat(outs), "lse": torch.cat(lses)}
+
+
+# ---------------------------------------------------------------------------
+# The framework's operators
+# ---------------------------------------------------------------------------
+
+def _kvq_cache(case, x):
+    from bit_kv_cache_16_b200 import kvq
+
+    cap = max(n + m for n, m in zip(x["held"], x["new"]))
+    if case["paged"]:
+        cache = kvq.Cache(case["fmt"], case["batch"], case["hq"], case["hkv"], x["pages"] * 16, 16, case["residual"],
+                          page_size=16, max_pages_per_seq=x["pages"], num_pages=x["pool"])
+        cache.set_page_table(x["table"])
+        return cache
+    unit = 16 if case["fmt"] in (8, 16) else case["group"]
+    cap = max(unit, -(-cap // unit) * unit)
+    return kvq.Cache(case["fmt"], case["batch"], case["hq"], case["hkv"], cap, case["group"], case["residual"])
+
+
+def _prepare_own(case, x, st):
+    c = st["kvq"] = _kvq_cache(case, x)
+    held, new = x["held"], x["new"]
+    st["cu"], st["cu_new"] = _offsets(held), _offsets(new)
+    st["total"] = _offsets([n + m for n, m in zip(held, new)])
+    if case["fmt"] == 8:
+        c.region("fp8_scale").view(torch.float32).copy_(x["scale"].flatten())
+    if case["op"] == "write":
+        rows = sum(held) + sum(new)
+        st["out"] = [torch.empty(rows, case["hkv"], D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        return
+    c.append_chunk(x["k"], x["v"], st["cu"], max(held), token_class=x["cls"] if case["fmt"] == 6 else None)
+    if case["op"] == "read":
+        st["out"] = [torch.empty_like(x["k"]), torch.empty_like(x["v"])]
+    elif case["op"] == "chunk":
+        st["out"] = torch.empty_like(x["q"])
+        n = c.chunk_workspace_bytes(0, sum(new), max(new), max(held), case["window"], case["sinks"])
+        st["ws"] = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    else:
+        st["out"] = torch.empty(case["batch"], case["hq"], D, device="cuda")
+        st["lse"] = torch.empty(case["batch"], case["hq"], device="cuda")
+        n = c.window_workspace_bytes(0, max(held), case["window"], case["sinks"])
+        st["ws"] = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+
+
+def _run_own(st):
+    case, x, c = st["case"], st["x"], st["kvq"]
+    held, new = x["held"], x["new"]
+    if case["op"] == "write":
+        mixed = case["fmt"] == 6
+        c.reset()
+        c.append_chunk(x["k"], x["v"], st["cu"], max(held), token_class=x["cls"] if mixed else None)
+        c.append_chunk(x["k_new"], x["v_new"], st["cu_new"], max(new), token_class=x["cls_new"] if mixed else None)
+        k, v = st["out"]
+        c.read_tokens(None, st["total"], max(n + m for n, m in zip(held, new)), k, v)
+        return {"k": k, "v": v, "seq_len": c.seq_len(), "n_quant": c.n_quant()}
+    if case["op"] == "read":
+        k, v = st["out"]
+        c.read_tokens(None, st["cu"], max(held), k, v)
+        return {"k": k, "v": v}
+    if case["op"] == "chunk":
+        c.chunk_attention(x["q"], x["k_new"], x["v_new"], st["cu_new"], max(new), st["out"], SCALE, st["ws"], 0,
+                          max(held), window=case["window"], sinks=case["sinks"])
+        return st["out"]
+    c.decode_attention_window(x["q"], st["out"], SCALE, case["window"], case["sinks"], st["ws"], 0, max(held),
+                              lse=st["lse"])
+    return {"out": st["out"], "lse": st["lse"]}
+
+
+def prepare(case, seed):
+    x = _inputs(case, seed)
+    st = {"case": case, "x": x}
+    if own:
+        _prepare_own(case, x, st)
+        return st
+    if case["op"] == "write":
+        # where each sequence's rows stand in the two pieces laid end to end
+        order, at, at_new = [], 0, sum(x["held"])
+        for n, m in zip(x["held"], x["new"]):
+            order += [torch.arange(at, at + n), torch.arange(at_new, at_new + m)]
+            at, at_new = at + n, at_new + m
+        st["order"] = torch.cat(order).cuda()
+    else:
+        st["cache"] = _held(case, x, x["held"], x["k"], x["v"], x["cls"])
+        st["plan"] = _plan(case, x, st["cache"])
+    return st
+
+
+def run(state):
+    if own:
+        return _run_own(state)
+    return _run_plain(state)
+
+
+# ---------------------------------------------------------------------------
+# The definition in 64 bits
+# ---------------------------------------------------------------------------
+
+def _exact_set(x, levels, dim):
+    """x^ in 64 bits of sets along `dim` (32- and 16-bit roundings only where the encoder's definition has them)."""
+    x = x.double()
+    lo, hi = x.min(dim, True).values, x.max(dim, True).values
+    s = ((hi - lo).float().double() / levels).float().half().double()
+    z = lo.half().double()
+    inv = torch.where(s > 0, (1.0 / s).float().double(), 0.0)
+    t = ((x - z).float().double() * inv).float().double()
+    return torch.clamp(torch.round(t), min=torch.zeros_like(lo), max=torch.zeros_like(lo) + levels) * s + z
+
+
+def _exact_rows(case, x, k, v, cls):
+    """64-bit keys and values of one sequence as the cache holds them."""
+    n, G, fmt = k.shape[0], case["group"], case["fmt"]
+    if fmt == 8:
+        got = []
+        for rows, scale in zip((k, v), x["scale"]):
+            y = (rows.double() * (1.0 / scale.double()).float().double()[:, None]).float()
+            got.append(y.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).double() * scale.double()[:, None])
+        return got
+    if fmt == 16:
+        return [_exact_set(rows, 255.0, 2) for rows in (k, v)]
+    q = _quantized(case, n)
+    kq, vq = k.double(), v.double()
+    if q:
+        if fmt == 6:
+            top = torch.where(cls[:q].reshape(-1, G).max(1).values == 4, 15.0, 3.0).double()
+        else:
+            top = torch.full((q // G,), 2.0 ** fmt - 1.0, device="cuda", dtype=torch.float64)
+        groups = k[:q].reshape(q // G, G, *k.shape[1:])
+        kq[:q] = _exact_set(groups, top.view(-1, 1, 1, 1), 1).reshape(q, *k.shape[1:])
+        vq[:q] = _exact_set(v[:q], top.repeat_interleave(G).view(-1, 1, 1), 2)
+    return [kq, vq]
+
+
+def exact(case, seed):
+    x = _inputs(case, seed)
+    parts = [torch.split(x[n], x["held"]) for n in ("k", "v", "cls")]
+    news = [torch.split(x[n], x["new"]) for n in ("k_new", "v_new", "cls_new")]
+    ks, vs, outs, lses = [], [], [], []
+    group = case["hq"] // case["hkv"]
+    at = 0
+    for b, (n, m) in enumerate(zip(x["held"], x["new"])):
+        k, v, cls = (p[b] for p in parts)
+        if case["op"] in ("write", "read"):
+            if case["op"] == "write":
+                k, v, cls = (torch.cat([a, p[b]]) for a, p in zip((k, v, cls), news))
+            k, v = _exact_rows(case, x, k, v, cls)
+            ks.append(k)
+            vs.append(v)
+            continue
+        k, v = _exact_rows(case, x, k, v, cls)
+        k, v = torch.cat([k, news[0][b].double()]), torch.cat([v, news[1][b].double()])
+        chunk = case["op"] == "chunk"
+        q = x["q"][at:at + m] if chunk else x["q"][b:b + 1]
+        at += m
+        row = torch.arange(n, n + m, device="cuda") if chunk else torch.tensor([n - 1], device="cuda")
+        col = torch.arange(n + m, device="cuda")
+        hidden = col[None, :] > row[:, None]
+        if case["window"]:
+            hidden |= (col[None, :] <= row[:, None] - case["window"]) & (col[None, :] >= case["sinks"])
+        o, l = [], []
+        for h in range(case["hq"]):
+            score = (q[:, h].double() @ k[:, h // group].T) / math.sqrt(D)
+            score[hidden] = -math.inf
+            l.append(torch.logsumexp(score, 1))
+            o.append(torch.exp(score - l[-1][:, None]) @ v[:, h // group])
+        outs.append(torch.stack(o, 1))
+        lses.append(torch.stack(l, 1))
+    if case["op"] == "write":
+        return {"k": torch.cat(ks), "v": torch.cat(vs), "seq_len": None, "n_quant": None}
+    if case["op"] == "read":
+        return {"k": torch.cat(ks), "v": torch.cat(vs)}
+    if case["op"] == "chunk":
+        return torch.cat(outs)
+    return {"out": torch.cat(outs), "lse": torch.cat(lses)}
