@@ -435,7 +435,8 @@ def _run_own(st):
         c.append_chunk(x["k_new"], x["v_new"], st["cu_new"], max(new), token_class=x["cls_new"] if mixed else None)
         k, v = st["out"]
         c.read_tokens(None, st["total"], max(n + m for n, m in zip(held, new)), k, v)
-        return {"k": k, "v": v, "seq_len": c.seq_len(), "n_quant": c.n_quant()}
+        B = case["batch"]                  # the counters' buffers are padded to 16 bytes
+        return {"k": k, "v": v, "seq_len": c.seq_len()[:B], "n_quant": c.n_quant()[:B]}
     if case["op"] == "read":
         k, v = st["out"]
         c.read_tokens(None, st["cu"], max(held), k, v)
