@@ -2,7 +2,7 @@
 // entry point checks its arguments before enqueuing anything.
 #include <string.h>
 
-#include "kvq_common.cuh"
+#include "kvq_chunk.cuh"
 
 namespace kvq {
 cudaError_t launch_prefill(const kvq_cache& c, const void* k, const void* v, const int32_t* cu, int max_len,
@@ -18,6 +18,13 @@ cudaError_t launch_decode(const kvq_cache& c, const void* q, float* out, float* 
                           int num_splits, cudaStream_t st);
 cudaError_t launch_merge(const float* outs, const float* lses, int parts, long long rows, float* out, float* lse_out,
                          cudaStream_t st);
+cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v, const uint8_t* cls,
+                                const int32_t* cu, int max_new, cudaStream_t st);
+cudaError_t launch_read_tokens(const kvq_cache& c, const int32_t* start, const int32_t* cu, int max_len, void* k,
+                               void* v, cudaStream_t st);
+cudaError_t launch_chunk_attention(const ChunkAttnArgs& A, cudaStream_t st);
+int chunk_default_splits(const kvq_shape& s, int rows, int max_new, int max_len, int window, int sinks);
+size_t chunk_workspace_bytes(const kvq_shape& s, int num_splits, int rows);
 int decode_default_splits(const kvq_shape& s, int max_len);
 size_t decode_workspace_bytes(const kvq_shape& s, int num_splits);
 }  // namespace kvq
@@ -229,6 +236,85 @@ kvq_status kvq_append_flush_mixed(kvq_cache* cache, const void* k_new_bf16, cons
   kvq_status st = kvq_append_token_mixed(cache, k_new_bf16, v_new_bf16, token_class_dev, stream);
   if (st != KVQ_OK) return st;
   return from_cuda(launch_flush(*cache, (cudaStream_t)stream));
+}
+
+kvq_status kvq_append_chunk(kvq_cache* cache, const void* k_new_bf16, const void* v_new_bf16,
+                            const uint8_t* token_class_dev, const int32_t* cu_seqlens_dev, int32_t max_new,
+                            kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!cu_seqlens_dev || max_new < 0) return KVQ_ERR_INVALID_ARG;
+  const bool mixed = is_mixed(cache->shape.format);
+  if (max_new > 0 && (!k_new_bf16 || !v_new_bf16 || (mixed && !token_class_dev))) return KVQ_ERR_INVALID_ARG;
+  if (!mixed && token_class_dev) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(k_new_bf16) || !aligned16(v_new_bf16) || ((uintptr_t)cu_seqlens_dev & 3u)) return KVQ_ERR_ALIGNMENT;
+  return from_cuda(
+      launch_append_chunk(*cache, k_new_bf16, v_new_bf16, token_class_dev, cu_seqlens_dev, max_new, (cudaStream_t)stream));
+}
+
+kvq_status kvq_read_tokens(const kvq_cache* cache, const int32_t* start_dev, const int32_t* cu_seqlens_dev,
+                           int32_t max_len, void* k_bf16, void* v_bf16, kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!cu_seqlens_dev || max_len < 0 || (max_len > 0 && !k_bf16 && !v_bf16)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(k_bf16) || !aligned16(v_bf16) || ((uintptr_t)cu_seqlens_dev & 3u) || ((uintptr_t)start_dev & 3u))
+    return KVQ_ERR_ALIGNMENT;
+  return from_cuda(
+      launch_read_tokens(*cache, start_dev, cu_seqlens_dev, max_len, k_bf16, v_bf16, (cudaStream_t)stream));
+}
+
+// Split count of a chunk attention call (0 = the library's choice), or 0 if
+// an argument is out of range.
+static int chunk_splits(const kvq_shape& s, int32_t num_splits, int32_t total_new, int32_t max_new, int32_t max_len,
+                        int32_t window, int32_t sinks) {
+  if (num_splits < 0 || num_splits > 65535 || total_new < 0 || max_new < 0 || max_len < 0 || window < 0 || sinks < 0)
+    return 0;
+  if (num_splits > 0) return num_splits;
+  return chunk_default_splits(s, total_new, min(max_new, total_new), min(max_len, s.capacity), window, sinks);
+}
+
+size_t kvq_chunk_workspace_bytes(const kvq_cache* cache, int32_t num_splits, int32_t total_new, int32_t max_new,
+                                 int32_t max_len, int32_t window, int32_t sinks) {
+  if (!cache || check_shape(&cache->shape) != KVQ_OK) return 0;
+  const int splits = chunk_splits(cache->shape, num_splits, total_new, max_new, max_len, window, sinks);
+  return splits ? chunk_workspace_bytes(cache->shape, splits, total_new) : 0;
+}
+
+kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q_bf16, const void* k_new_bf16,
+                               const void* v_new_bf16, const int32_t* cu_seqlens_dev, int32_t total_new,
+                               int32_t max_new, float softmax_scale, int32_t window, int32_t sinks, void* out_bf16,
+                               void* workspace, size_t ws_bytes, int32_t num_splits, int32_t max_len,
+                               kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!cu_seqlens_dev || !(softmax_scale == softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  const kvq_shape& s = cache->shape;
+  const int splits = chunk_splits(s, num_splits, total_new, max_new, max_len, window, sinks);
+  if (!splits) return KVQ_ERR_INVALID_ARG;
+  if (total_new > 0 && (!q_bf16 || !k_new_bf16 || !v_new_bf16 || !out_bf16)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(k_new_bf16) || !aligned16(v_new_bf16) || !aligned16(out_bf16) ||
+      !aligned16(workspace) || ((uintptr_t)cu_seqlens_dev & 3u))
+    return KVQ_ERR_ALIGNMENT;
+  const size_t need = chunk_workspace_bytes(s, splits, total_new);
+  if (need > 0 && !workspace) return KVQ_ERR_INVALID_ARG;
+  if (ws_bytes < need) return KVQ_ERR_WORKSPACE;
+  if (total_new == 0) return KVQ_OK;
+  ChunkAttnArgs A;
+  A.c = *cache;
+  A.q = (const uint16_t*)q_bf16;
+  A.k = (const uint16_t*)k_new_bf16;
+  A.v = (const uint16_t*)v_new_bf16;
+  A.cu = cu_seqlens_dev;
+  A.out = (uint16_t*)out_bf16;
+  A.ws_o = (float*)workspace;
+  A.ws_ml = nullptr;
+  A.scale_log2 = softmax_scale * 1.4426950408889634f;
+  A.rows = total_new;
+  A.max_new = max_new;
+  A.window = window;
+  A.sinks = sinks;
+  A.splits = splits;
+  return from_cuda(launch_chunk_attention(A, (cudaStream_t)stream));
 }
 
 int32_t kvq_decode_default_splits(const kvq_cache* cache, int32_t max_len) {

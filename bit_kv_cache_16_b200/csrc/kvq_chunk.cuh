@@ -1,0 +1,64 @@
+// Shared pieces of the chunk attention kernels (kvq_chunk.cu, kvq_chunk_mma.cu).
+#pragma once
+
+#include "kvq_common.cuh"
+
+namespace kvq {
+
+struct ChunkAttnArgs {
+  kvq_cache c;
+  const uint16_t* q;      // bf16 [rows][H_q][128]
+  const uint16_t* k;      // bf16 [rows][H_kv][128]: the chunk's own keys
+  const uint16_t* v;      // bf16 [rows][H_kv][128]
+  const int32_t* cu;      // [B + 1] chunk rows of each sequence
+  uint16_t* out;          // bf16 [rows][H_q][128]
+  float* ws_o;            // [splits][rows][H_q][128] (splits > 1)
+  float* ws_ml;           // [splits][rows][H_q][2]
+  float scale_log2;       // softmax_scale * log2(e)
+  int rows;               // rows of the chunk arrays
+  int max_new;
+  int window, sinks;      // window 0: every earlier token is visible
+  int splits;
+};
+
+// The sequence's share of a chunk: cached tokens n (nq quantized), new tokens
+// m, its rows from t0 on.  ok is false (and nothing is computed) for a state,
+// length or row range that fails the checks; err is the bit to report.
+struct ChunkSeq {
+  int n, nq, m, t0;
+  uint32_t err;
+};
+
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkAttnArgs& A, int b) {
+  ChunkSeq q;
+  q.t0 = A.cu[b];
+  q.m = A.cu[b + 1] - q.t0;
+  q.n = A.c.seq_len[b];
+  q.nq = A.c.n_quant[b];
+  q.err = 0u;
+  if (state_bad(A.c.shape, q.n, q.nq)) q.err = KVQ_DEVERR_STATE;
+  else if (q.m < 0 || q.m > A.max_new || q.t0 < 0 || q.t0 > A.rows - q.m) q.err = KVQ_DEVERR_PREFILL_LEN;
+  if (q.err) q.m = 0;
+  return q;
+}
+
+// Key tiles of TS tokens that rows at positions [p0, p1] can see, in order:
+// the tiles of the first `sinks` tokens, then those from the first row's
+// window to p1.  tile(i) for 0 <= i < count.
+struct TileRange {
+  int lead, skip, count;
+  __device__ __forceinline__ TileRange(int p0, int p1, int window, int sinks, int TS) {
+    const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
+    skip = lo / TS;
+    lead = min(skip, (min(sinks, lo) + TS - 1) / TS);
+    count = lead + p1 / TS + 1 - skip;
+  }
+  __device__ __forceinline__ int tile(int i) const { return i < lead ? i : skip + i - lead; }
+};
+
+// Key t is visible to the row at position p.
+__device__ __forceinline__ bool key_visible(int t, int p, int window, int sinks) {
+  return t <= p && (window <= 0 || t > p - window || t < sinks);
+}
+
+}  // namespace kvq

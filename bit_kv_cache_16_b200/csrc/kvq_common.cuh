@@ -74,6 +74,17 @@ struct Addr {
   }
 };
 
+// A (seq_len, n_quant) pair no prefill, append or flush can produce.
+__device__ __forceinline__ bool state_bad(const kvq_shape& s, int n, int nq) {
+  if (is_token_cache(s.format)) return n < 0 || nq != n || n > s.capacity;
+  return n < 0 || nq < 0 || nq > n || nq > s.capacity || (nq & (s.group - 1)) || n - nq > window_slots(s);
+}
+// 16-token tiles of a quantized part of nq tokens (FP8 and INT8: the last one
+// may be partial; INT2/4: nq is a whole number of groups).
+__device__ __forceinline__ int quant_tiles(const kvq_shape& s, int nq) {
+  return is_token_cache(s.format) ? (nq + kTile - 1) / kTile : nq / kTile;
+}
+
 // Position of channel c in a key scale/zero row (the decode's pair order,
 // include/kvq.h).
 template <int BITS>

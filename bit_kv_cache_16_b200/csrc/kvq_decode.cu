@@ -859,17 +859,6 @@ __device__ __forceinline__ void window_chunk_int(const kvq_cache& c, int b, int 
 // p_last(u) + u, with p_first/p_last the owners of its first and last chunk
 // (skipping warps whose range is empty, which write nothing).
 
-// A (seq_len, n_quant) pair no prefill, append or flush can produce.
-__device__ __forceinline__ bool state_bad(const kvq_shape& s, int n, int nq) {
-  if (is_int8(s.format)) return n < 0 || nq != n || n > s.capacity;
-  return n < 0 || nq < 0 || nq > n || nq > s.capacity || (nq & (s.group - 1)) || n - nq > window_slots(s);
-}
-// 16-token tiles of a quantized part of nq tokens (INT8: the last one may
-// be partial; INT2/4: nq is a whole number of groups).
-__device__ __forceinline__ int quant_tiles(const kvq_shape& s, int nq) {
-  return is_int8(s.format) ? (nq + kTile - 1) / kTile : nq / kTile;
-}
-
 // Chunks of sequence b's quantized part (0 for a state that fails the checks).
 __device__ __forceinline__ int seq_chunks(const kvq_cache& c, int b) {
   const kvq_shape& s = c.shape;

@@ -1,0 +1,85 @@
+// kvq_read_tokens: token ranges of the cache as bf16 rows.
+#include "kvq_rows.cuh"
+
+namespace kvq {
+
+struct ReadArgs {
+  kvq_cache c;
+  const int32_t* start;    // [B] first token per sequence, or null (0)
+  const int32_t* cu;       // [B + 1] output rows
+  uint16_t* k;             // bf16 [rows][H_kv][128], or null
+  uint16_t* v;             // same, or null
+  int max_len;
+};
+
+// Grid (pairs of tiles, H_kv, B), 128 threads: two 16-token tiles of one
+// (sequence, kv head), warps 0 and 1 their keys, warps 2 and 3 their values.
+// A tile is either quantized (tokens below n_quant, a multiple of 16 where
+// there is a window) or held in the window ring.  Bound by the bf16 rows it
+// writes; every output row is written in whole 32-byte sectors.
+template <int FMT>
+__global__ void __launch_bounds__(128) read_tokens_kernel(ReadArgs A) {
+  const kvq_cache& c = A.c;
+  const kvq_shape& s = c.shape;
+  const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = A.cu[b], len = A.cu[b + 1] - row0;
+  const int first = A.start ? A.start[b] : 0;
+  const int n = c.seq_len[b], nq = c.n_quant[b];
+  const bool lead = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
+  if (state_bad(s, n, nq)) {
+    if (lead) atomicOr(c.err_word, KVQ_DEVERR_STATE);
+    return;
+  }
+  if (len < 0 || len > A.max_len || first < 0 || first > n || len > n - first) {
+    if (lead) atomicOr(c.err_word, KVQ_DEVERR_PREFILL_LEN);
+    return;
+  }
+  const int tile = first / kTile + 2 * blockIdx.x + (warp & 1);
+  const int lo = max(first - tile * kTile, 0), hi = min(kTile, first + len - tile * kTile);
+  if (lo >= hi) return;
+  const bool key = warp < 2;
+  uint16_t* out = key ? A.k : A.v;
+  if (!out) return;
+  // row of the tile's token 0 (never written when lo > 0)
+  out += ((int64_t)(row0 + tile * kTile - first) * s.num_kv_heads + h) * kHeadDim;
+  const int64_t stride = (int64_t)s.num_kv_heads * kHeadDim;
+  if (!is_token_cache(s.format) && tile * kTile >= nq) {
+    const int Ws = window_slots(s);
+    const uint16_t* ring = (const uint16_t*)(key ? c.k_res : c.v_res) + Addr::ring_row(s, b, h, 0);
+    for (int r = lo + (lane >> 4); r < hi; r += 2)
+      *reinterpret_cast<uint4*>(out + r * stride + 8 * (lane & 15)) =
+          *reinterpret_cast<const uint4*>(ring + (size_t)((tile * kTile + r) % Ws) * kHeadDim + 8 * (lane & 15));
+    return;
+  }
+  TileSrc d;
+  if (!tile_src<FMT>(c, b, h, tile, d)) {
+    if (lane == 0) atomicOr(c.err_word, KVQ_DEVERR_PAGE_RANGE);
+    return;
+  }
+  auto put = [&](int r, int ch, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(out + r * stride + ch) =
+        make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+  };
+  if (key) key_rows<FMT>(d, lo, hi, put);
+  else value_rows<FMT>(d, lo, hi, put);
+}
+
+cudaError_t launch_read_tokens(const kvq_cache& c, const int32_t* start, const int32_t* cu, int max_len, void* k,
+                               void* v, cudaStream_t st) {
+  const kvq_shape& s = c.shape;
+  const ReadArgs A{c, start, cu, (uint16_t*)k, (uint16_t*)v, max_len};
+  const int most = min(max_len, s.capacity);         // longer ranges are rejected on the device
+  // a range of m tokens touches at most (m + 30) / 16 tiles
+  dim3 grid(((most + 2 * kTile - 2) / kTile + 1) / 2, s.num_kv_heads, s.batch);
+  if (grid.x == 0) grid.x = 1;
+  switch (s.format) {
+    case KVQ_FORMAT_INT2: read_tokens_kernel<2><<<grid, 128, 0, st>>>(A); break;
+    case KVQ_FORMAT_INT4: read_tokens_kernel<4><<<grid, 128, 0, st>>>(A); break;
+    case KVQ_FORMAT_MIXED: read_tokens_kernel<6><<<grid, 128, 0, st>>>(A); break;
+    case KVQ_FORMAT_FP8_E4M3: read_tokens_kernel<8><<<grid, 128, 0, st>>>(A); break;
+    default: read_tokens_kernel<16><<<grid, 128, 0, st>>>(A); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace kvq

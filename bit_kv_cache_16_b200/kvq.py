@@ -7,6 +7,7 @@ of the library fails loudly: there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -40,6 +41,7 @@ REGIONS = ["k_codes", "k_meta", "v_codes", "v_meta", "k_res", "v_res", "seq_len"
 
 EXPORTED = ["kvq_buffer_bytes", "kvq_quantize_prefill", "kvq_append_token", "kvq_flush_group", "kvq_append_flush",
             "kvq_quantize_prefill_mixed", "kvq_append_token_mixed", "kvq_append_flush_mixed",
+            "kvq_append_chunk", "kvq_read_tokens", "kvq_chunk_attention", "kvq_chunk_workspace_bytes",
             "kvq_decode_attention", "kvq_decode_attention_lse", "kvq_merge_partials",
             "kvq_decode_attention_noalloc", "kvq_decode_workspace_bytes", "kvq_decode_default_splits",
             "kvq_read_error", "kvq_status_string", "kvq_version"]
@@ -86,6 +88,10 @@ def load(path: Optional[str] = None):
         "kvq_quantize_prefill_mixed": (i32, [pc, vp, vp, vp, vp, i32, vp]),
         "kvq_append_token_mixed": (i32, [pc, vp, vp, vp, vp]),
         "kvq_append_flush_mixed": (i32, [pc, vp, vp, vp, vp]),
+        "kvq_append_chunk": (i32, [pc, vp, vp, vp, vp, i32, vp]),
+        "kvq_read_tokens": (i32, [pc, vp, vp, i32, vp, vp, vp]),
+        "kvq_chunk_attention": (i32, [pc, vp, vp, vp, vp, i32, i32, f32, i32, i32, vp, vp, sz, i32, i32, vp]),
+        "kvq_chunk_workspace_bytes": (sz, [pc, i32, i32, i32, i32, i32, i32]),
         "kvq_decode_attention": (i32, [pc, vp, vp, f32, vp, sz, i32, i32, vp]),
         "kvq_decode_attention_lse": (i32, [pc, vp, vp, vp, f32, vp, sz, i32, i32, vp]),
         "kvq_merge_partials": (i32, [vp, vp, i32, ctypes.c_int64, vp, vp, vp]),
@@ -180,6 +186,37 @@ def kvq_append_token_mixed(cache: KvqCache, k_new, v_new, token_class, stream=No
 def kvq_append_flush_mixed(cache: KvqCache, k_new, v_new, token_class, stream=None):
     _check("kvq_append_flush_mixed", load().kvq_append_flush_mixed(ctypes.byref(cache), _ptr(k_new), _ptr(v_new),
                                                                    _ptr(token_class), _stream(stream)))
+
+
+def kvq_append_chunk(cache: KvqCache, k_new, v_new, token_class, cu_seqlens, max_new: int, stream=None):
+    """Append a ragged chunk of new tokens (token_class: MIXED only, else None)."""
+    _check("kvq_append_chunk",
+           load().kvq_append_chunk(ctypes.byref(cache), _ptr(k_new), _ptr(v_new), _ptr(token_class),
+                                   _ptr(cu_seqlens), int(max_new), _stream(stream)))
+
+
+def kvq_read_tokens(cache: KvqCache, start, cu_seqlens, max_len: int, k_out, v_out, stream=None):
+    """Token ranges of the cache as bf16 rows (start None: from token 0; k_out or v_out None: not read)."""
+    _check("kvq_read_tokens",
+           load().kvq_read_tokens(ctypes.byref(cache), _ptr(start), _ptr(cu_seqlens), int(max_len), _ptr(k_out),
+                                  _ptr(v_out), _stream(stream)))
+
+
+def kvq_chunk_attention(cache: KvqCache, q, k_new, v_new, cu_seqlens, total_new: int, max_new: int,
+                        softmax_scale: float, window: int, sinks: int, out, workspace, ws_bytes: int,
+                        num_splits: int, max_len: int, stream=None):
+    """A chunk of new tokens attends to the cache and, causally, to itself."""
+    _check("kvq_chunk_attention",
+           load().kvq_chunk_attention(ctypes.byref(cache), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cu_seqlens),
+                                      int(total_new), int(max_new), float(softmax_scale), int(window), int(sinks),
+                                      _ptr(out), _ptr(workspace), int(ws_bytes), int(num_splits), int(max_len),
+                                      _stream(stream)))
+
+
+def kvq_chunk_workspace_bytes(cache: KvqCache, num_splits: int, total_new: int, max_new: int, max_len: int,
+                              window: int = 0, sinks: int = 0) -> int:
+    return int(load().kvq_chunk_workspace_bytes(ctypes.byref(cache), int(num_splits), int(total_new), int(max_new),
+                                                int(max_len), int(window), int(sinks)))
 
 
 def kvq_decode_workspace_bytes(cache: KvqCache, num_splits: int, max_len: int) -> int:
@@ -300,6 +337,79 @@ class Cache:
 
     def append_flush_mixed(self, k_new, v_new, token_class, stream=None):
         kvq_append_flush_mixed(self.desc, k_new, v_new, token_class, stream)
+
+    # The calls below check their tensors (device, element size, layout and
+    # shape) and run on the cache's device, whatever the current one is.
+
+    def _need(self, name: str, t, shape, itemsize: int):
+        """t is a contiguous tensor on the cache's device, of this element size and shape (None: any extent)."""
+        if t.device.type != self.device.type or (self.device.index is not None and t.device != self.device):
+            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, self.device))
+        if t.element_size() != itemsize:
+            raise ValueError("%s has elements of %d bytes, not %d" % (name, t.element_size(), itemsize))
+        if not t.is_contiguous():
+            raise ValueError("%s is not contiguous" % name)
+        if len(shape) != t.dim() or any(e is not None and e != d for e, d in zip(shape, t.shape)):
+            raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape),
+                                                         tuple("*" if e is None else e for e in shape)))
+
+    def _guard(self, stream):
+        """(a context in which the cache's device is current, the stream to use)."""
+        dev = self.buffers["seq_len"].device
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        return (contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)), stream
+
+    def reset(self):
+        """Empty the cache: every sequence has no token (the FP8 scales stay)."""
+        self.seq_len().zero_()
+        self.n_quant().zero_()
+
+    def append_chunk(self, k_new, v_new, cu_seqlens, max_new: int, token_class=None, stream=None):
+        """Append a ragged chunk: k_new, v_new bf16 [T, H_kv, 128], cu_seqlens int32 [B + 1]."""
+        s = self.shape
+        self._need("k_new", k_new, (None, s.num_kv_heads, 128), 2)
+        self._need("v_new", v_new, tuple(k_new.shape), 2)
+        self._need("cu_seqlens", cu_seqlens, (s.batch + 1,), 4)
+        if token_class is not None:
+            self._need("token_class", token_class, (k_new.shape[0],), 1)
+        ctx, stream = self._guard(stream)
+        with ctx:
+            kvq_append_chunk(self.desc, k_new, v_new, token_class, cu_seqlens, max_new, stream)
+
+    def read_tokens(self, start, cu_seqlens, max_len: int, k_out, v_out, stream=None):
+        """Tokens [start, start + length) of every sequence as bf16 rows [T, H_kv, 128] (start None: 0; either output
+        may be None)."""
+        s = self.shape
+        if start is not None:
+            self._need("start", start, (s.batch,), 4)
+        self._need("cu_seqlens", cu_seqlens, (s.batch + 1,), 4)
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
+                self._need(name, t, (None, s.num_kv_heads, 128), 2)
+        ctx, stream = self._guard(stream)
+        with ctx:
+            kvq_read_tokens(self.desc, start, cu_seqlens, max_len, k_out, v_out, stream)
+
+    def chunk_workspace_bytes(self, num_splits: int, total_new: int, max_new: int, max_len: int, window: int = 0,
+                              sinks: int = 0) -> int:
+        return kvq_chunk_workspace_bytes(self.desc, num_splits, total_new, max_new, max_len, window, sinks)
+
+    def chunk_attention(self, q, k_new, v_new, cu_seqlens, max_new: int, out, softmax_scale: float, workspace,
+                        num_splits: int, max_len: int, window: int = 0, sinks: int = 0, stream=None):
+        """out bf16 [T, H_q, 128]: the chunk's queries q over the cached tokens and, causally, over k_new, v_new."""
+        s = self.shape
+        rows = q.shape[0]
+        self._need("q", q, (None, s.num_q_heads, 128), 2)
+        self._need("k_new", k_new, (rows, s.num_kv_heads, 128), 2)
+        self._need("v_new", v_new, (rows, s.num_kv_heads, 128), 2)
+        self._need("out", out, (rows, s.num_q_heads, 128), 2)
+        self._need("cu_seqlens", cu_seqlens, (s.batch + 1,), 4)
+        n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ctx, stream = self._guard(stream)
+        with ctx:
+            kvq_chunk_attention(self.desc, q, k_new, v_new, cu_seqlens, rows, max_new, softmax_scale, window, sinks,
+                                out, workspace, n, num_splits, max_len, stream)
 
     def workspace_bytes(self, num_splits: int, max_len: int) -> int:
         return kvq_decode_workspace_bytes(self.desc, num_splits, max_len)

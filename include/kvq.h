@@ -387,6 +387,96 @@ kvq_status kvq_decode_attention_lse(const kvq_cache *cache, const void *q_bf16, 
 kvq_status kvq_merge_partials(const float *outs, const float *lses, int32_t parts, int64_t rows,
                               float *out, float *lse_out, kvq_stream_t stream);
 
+/*
+ * Append a chunk of new tokens to every sequence: a piece of a prompt behind
+ * the pieces already cached (chunked prefill), the accepted tokens of a
+ * speculative step, or a whole prompt into an emptied cache.  The state
+ * afterwards is the one that kvq_append_flush, called once per token, would
+ * leave (section 3.2 of the arganzheng page): seq_len += m,
+ * n_quant = G*floor(max(seq_len - R, 0)/G) (seq_len for FP8 and INT8), with
+ * the same codes, scales and window slots, bit for bit.
+ *  k_new_bf16, v_new_bf16: bf16 [T_total][H_kv][D], the sequences' chunks
+ *                  back to back; may be NULL when max_new is 0.
+ *  token_class_dev: MIXED: uint8 [T_total], as kvq_quantize_prefill_mixed;
+ *                  NULL for every other format.
+ *  cu_seqlens_dev: int32 [B+1] device array, sequence b's chunk is rows
+ *                  [cu[b], cu[b+1]); chunks may be empty.
+ *  max_new:        an upper bound of the chunk lengths (sizes the grid).
+ * FP8 encodes with the stored scales (saturating): they must be set, by an
+ * earlier prefill or by the caller.  A sequence's chunk is dropped whole, its
+ * state left as it was, if it is longer than max_new (KVQ_DEVERR_PREFILL_LEN),
+ * does not fit the capacity (KVQ_DEVERR_APPEND_FULL), needs a page whose id is
+ * out of range (KVQ_DEVERR_PAGE_RANGE) or finds an inconsistent state
+ * (KVQ_DEVERR_STATE).  Two launches; the second (counters) waits for the
+ * first on the device.
+ */
+kvq_status kvq_append_chunk(kvq_cache *cache, const void *k_new_bf16, const void *v_new_bf16,
+                            const uint8_t *token_class_dev, const int32_t *cu_seqlens_dev, int32_t max_new,
+                            kvq_stream_t stream);
+
+/*
+ * Read cached tokens back as bf16 rows: x^ = code * scale + zero in fp32 (the
+ * kept value itself for a dense-and-sparse cache), rounded once to bf16;
+ * window tokens as they were given.  Keys stored before RoPE come back
+ * un-rotated.
+ *  start_dev:      int32 [B] first token per sequence, or NULL (token 0).
+ *  cu_seqlens_dev: int32 [B+1]; output rows [cu[b], cu[b+1]) receive tokens
+ *                  start[b], start[b] + 1, ... of sequence b.
+ *  max_len:        an upper bound of the range lengths (sizes the grid).
+ *  k_bf16, v_bf16: bf16 [T_total][H_kv][D]; either may be NULL (not read).
+ * A range that is negative, longer than max_len or passes seq_len[b] sets
+ * KVQ_DEVERR_PREFILL_LEN, a bad page id KVQ_DEVERR_PAGE_RANGE (its 16 rows),
+ * an inconsistent state KVQ_DEVERR_STATE; the rows concerned, like rows that
+ * belong to no range, are left as they were.  One launch.
+ */
+kvq_status kvq_read_tokens(const kvq_cache *cache, const int32_t *start_dev, const int32_t *cu_seqlens_dev,
+                           int32_t max_len, void *k_bf16, void *v_bf16, kvq_stream_t stream);
+
+/*
+ * Attention of a chunk of new tokens over the packed cache and, causally,
+ * over the chunk itself: new token i of sequence b stands at position
+ * p = seq_len[b] + i, and for each query head h
+ *   out[row][h][:] = sum_t softmax_t(softmax_scale * q.k^_t) v^_t
+ * over the cached tokens t < seq_len[b] (dequantized; window tokens in bf16)
+ * and the chunk's own tokens t <= p (bf16, from k_new and v_new), kv head =
+ * h / (H_q / H_kv).  With window > 0 only the last `window` of them
+ * (t > p - window) and the first `sinks` tokens of the sequence (t < sinks)
+ * are visible.  The cache is only read: attend first, then add the chunk (or
+ * its accepted tokens) with kvq_append_chunk.  A chunk of one token per
+ * sequence is a decode step whose token is not yet in the cache.
+ *  q_bf16:         bf16 [total_new][H_q][D]
+ *  k_new_bf16, v_new_bf16: bf16 [total_new][H_kv][D] (with rope_theta > 0 keys
+ *                  before RoPE, as kvq_append_chunk takes them; they are
+ *                  rotated by their position here)
+ *  cu_seqlens_dev: int32 [B+1]; rows [cu[b], cu[b+1]) are sequence b's chunk
+ *                  (may be empty).  Rows in no chunk are left as they were.
+ *  total_new:      rows of q, k_new, v_new and out.
+ *  max_new:        an upper bound of the chunk lengths (sizes the grid).
+ *  window, sinks:  >= 0; window 0 = every earlier token is visible.
+ *  out_bf16:       bf16 [total_new][H_q][D]
+ *  workspace:      kvq_chunk_workspace_bytes(cache, num_splits, total_new,
+ *                  max_new, max_len, window, sinks) bytes; may be NULL if that
+ *                  is 0.  Nothing in it needs clearing; calls that overlap on
+ *                  the GPU need one each.
+ *  num_splits:     >= 1: each row's keys are cut into that many ranges, worked
+ *                  on by as many CTAs and merged by a second launch; 0 = the
+ *                  library's choice (few rows over a long cache are split).
+ *  max_len:        an upper bound of seq_len over the batch (for that choice).
+ * A sequence with an inconsistent state (KVQ_DEVERR_STATE) or a chunk longer
+ * than max_new or outside [0, total_new) (KVQ_DEVERR_PREFILL_LEN) is skipped,
+ * its rows left as they were; the tokens of a page whose id is out of range
+ * are left out (KVQ_DEVERR_PAGE_RANGE).
+ */
+kvq_status kvq_chunk_attention(const kvq_cache *cache, const void *q_bf16, const void *k_new_bf16,
+                               const void *v_new_bf16, const int32_t *cu_seqlens_dev, int32_t total_new,
+                               int32_t max_new, float softmax_scale, int32_t window, int32_t sinks,
+                               void *out_bf16, void *workspace, size_t ws_bytes, int32_t num_splits,
+                               int32_t max_len, kvq_stream_t stream);
+
+/* Workspace bytes kvq_chunk_attention needs (0 for bad arguments too). */
+size_t kvq_chunk_workspace_bytes(const kvq_cache *cache, int32_t num_splits, int32_t total_new, int32_t max_new,
+                                 int32_t max_len, int32_t window, int32_t sinks);
+
 /* Workspace bytes kvq_decode_attention needs for this split count (0 = the
  * library's choice for max_len). */
 size_t kvq_decode_workspace_bytes(const kvq_cache *cache, int32_t num_splits, int32_t max_len);

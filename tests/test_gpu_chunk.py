@@ -1,0 +1,468 @@
+"""Chunk append, read-back and chunk attention on the GPU against 64-bit references."""
+import numpy as np
+import pytest
+import torch
+
+from bit_kv_cache_16_b200 import kvq, synth
+
+from chunk_ref import HALF_BF16, attend, bf16, cached_rows, rotate
+from gpu_harness import (assert_fp8_state, assert_int8_state, assert_unit_state, make_gpu_cache, oracle_cache, round_up,
+                         to_dev)
+from layout import GpuState
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 1.0 / np.sqrt(128.0)
+
+
+def bits_of(x: np.ndarray) -> np.ndarray:
+    return torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+
+
+def cu_of(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+class Case:
+    """A cache filled by one append_chunk of w's tokens, and a ragged chunk behind it."""
+
+    def __init__(self, fmt, lens, new, hq=8, hkv=2, G=32, R=32, paged=False, rope=0.0, sparse=False, seed=0, extra=0,
+                 k_outlier=4.0):
+        self.fmt, self.lens, self.new = fmt, list(lens), list(new)
+        total = [n + m + extra for n, m in zip(self.lens, self.new)]
+        self.w = w = synth.make_workload("chunk", 9000 + seed, total, hq, hkv, fmt, G, R, page_size=16 if paged else 0,
+                                         k_outlier=k_outlier, q_outlier=1.0)
+        self.cache = make_gpu_cache(w, capacity=0 if paged else max(round_up(max(total), max(G, 16)), max(G, 16)),
+                                    rope_theta=rope, sparse=sparse)
+        self.classes = synth.token_classes(9000 + seed, total)
+        rows = [slice(w.cu_seqlens[b], w.cu_seqlens[b] + n) for b, n in enumerate(self.lens)]
+        fresh = [slice(r.stop, r.stop + m) for r, m in zip(rows, self.new)]
+        pick = lambda a, part: np.ascontiguousarray(np.concatenate([a[p] for p in part]))
+        self.k, self.v, self.cls = (pick(a, rows) for a in (w.k, w.v, self.classes))
+        self.kn, self.vn, self.clsn = (pick(a, fresh) for a in (w.k, w.v, self.classes))
+        rng = np.random.default_rng(seed)
+        self.q = bits_of(rng.standard_normal((sum(self.new), hq, 128)))
+        self.cu, self.cu_new = cu_of(self.lens), cu_of(self.new)
+        if fmt == 8:
+            amax = np.stack([np.abs(bf16(a)).max((0, 2)) for a in (w.k, w.v)]).astype(np.float32)
+            self.cache.region("fp8_scale").view(torch.float32).copy_(torch.from_numpy((amax / np.float32(448)).ravel()))
+
+    def append(self, k, v, cls, lens):
+        self.cache.append_chunk(to_dev(k), to_dev(v), cu_of(lens), max(lens),
+                                token_class=to_dev(cls) if self.fmt == 6 else None)
+
+    def fill(self):
+        self.append(self.k, self.v, self.cls, self.lens)
+        return self
+
+    def attend(self, splits=0, window=0, sinks=0, max_len=None, out=None, stream=None):
+        c, w = self.cache, self.w
+        rows = sum(self.new)
+        if out is None:
+            out = torch.full((rows, w.num_q_heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        max_len = max(self.lens) if max_len is None else max_len
+        n = c.chunk_workspace_bytes(splits, rows, max(self.new), max_len, window, sinks)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+        c.chunk_attention(to_dev(self.q), to_dev(self.kn), to_dev(self.vn), self.cu_new, max(self.new), out, SCALE, ws,
+                          splits, max_len, window=window, sinks=sinks, stream=stream)
+        torch.cuda.synchronize()
+        return out.float().cpu().numpy().astype(np.float64)
+
+    def check(self, out, window=0, sinks=0, rope=0.0, skip_pages=()):
+        st = GpuState(self.cache)
+        gq = self.w.num_q_heads // self.w.num_kv_heads
+        at = 0
+        for b, (n, m) in enumerate(zip(self.lens, self.new)):
+            for h in range(self.w.num_kv_heads):
+                if not m:
+                    continue
+                k, v = cached_rows(st, b, h, rope > 0, rope)
+                kn, vn = bf16(self.kn[at:at + m, h]), bf16(self.vn[at:at + m, h])
+                if rope > 0:
+                    kn = rotate(kn, np.arange(n, n + m, dtype=np.float64), rope)
+                k, v = np.concatenate([k, kn]), np.concatenate([v, vn])
+                present = np.ones(n + m, bool)
+                for bb, page in skip_pages:
+                    if bb == b:
+                        present[16 * page:16 * page + 16] = False
+                for g in range(gq):
+                    ref, _, tol = attend(bf16(self.q[at:at + m, h * gq + g]), k, v, np.arange(n, n + m), SCALE, window,
+                                         sinks, present)
+                    got = out[at:at + m, h * gq + g]
+                    err = np.abs(got - ref)
+                    assert np.all(err <= tol), (b, h, g, float(np.nanmax(err / tol)), int(np.isnan(got).sum()))
+            at += m
+
+
+FORMATS = [(2, 32, 128, False), (4, 32, 32, False), (4, 16, 16, True), (2, 16, 0, True), (4, 64, 0, False),
+           (2, 128, 100, False), (6, 32, 32, False), (6, 64, 16, False), (8, 32, 0, False), (16, 32, 0, False)]
+
+
+# ---------------------------------------------------------------------------
+# Append
+# ---------------------------------------------------------------------------
+
+def assert_state(case, oc):
+    torch.cuda.synchronize()
+    st = GpuState(case.cache)
+    units = [(b, h) for b in range(case.w.batch) for h in range(case.w.num_kv_heads)]
+    if case.fmt == 8:
+        assert_fp8_state(st, oc, units)
+    elif case.fmt == 16:
+        assert_int8_state(st, oc, units)
+    else:
+        for b, h in units:
+            assert_unit_state(st, oc, b, h)
+
+
+def oracle_of(case, lens):
+    """The oracle after a prefill of the first lens[b] tokens of every sequence."""
+    import dataclasses
+    w = case.w
+    part = [slice(w.cu_seqlens[b], w.cu_seqlens[b] + n) for b, n in enumerate(lens)]
+    pick = lambda a: np.ascontiguousarray(np.concatenate([a[p] for p in part]))
+    v = dataclasses.replace(w, lengths=np.asarray(lens), k=pick(w.k), v=pick(w.v),
+                            cu_seqlens=np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    return oracle_cache(v, case.cache.shape.capacity, classes=pick(case.classes),
+                        sparse=bool(case.cache.shape.sparse))
+
+
+@pytest.mark.parametrize("fmt,G,R,paged", [f for f in FORMATS if f[0] != 8])
+def test_append_chunk_state(fmt, G, R, paged):
+    """Pieces of every size, into empty and filled caches, leave the state of a prefill of all the tokens."""
+    lens = [0, 1, 15, 16, R + G - 1, R + G, 3 * G + R + 5, 500]
+    new = [1, 0, 17, G, 1, 2 * G + 3, R + G + 1, 401]
+    case = Case(fmt, lens, new, G=G, R=R, paged=paged, seed=fmt + G).fill()
+    assert_state(case, oracle_of(case, lens))
+    case.append(case.kn, case.vn, case.clsn, new)
+    assert_state(case, oracle_of(case, [n + m for n, m in zip(lens, new)]))
+    assert case.cache.error() == 0
+
+
+def test_append_chunk_fp8_scales():
+    """FP8: codes with the stored scales; the batch's own amax gives the prefill's codes."""
+    lens, new = [0, 1, 15, 16, 300], [1, 30, 17, 0, 77]
+    case = Case(8, lens, new, seed=3).fill()
+    case.append(case.kn, case.vn, case.clsn, new)
+    assert_state(case, oracle_of(case, [n + m for n, m in zip(lens, new)]))
+
+
+@pytest.mark.parametrize("sparse,G", [(True, 16), (True, 32), (False, 32)])
+def test_append_chunk_sparse_and_many_heads(sparse, G):
+    lens, new = [0, 77, 200], [100, 1, 90]
+    case = Case(4, lens, new, hq=20, hkv=10, G=G, R=32, sparse=sparse, seed=5).fill()
+    case.append(case.kn, case.vn, case.clsn, new)
+    assert_state(case, oracle_of(case, [n + m for n, m in zip(lens, new)]))
+
+
+@pytest.mark.parametrize("fmt,G,R", [(4, 32, 32), (2, 16, 100), (6, 32, 0), (16, 32, 0)])
+def test_append_chunk_in_pieces_equals_tokens(fmt, G, R):
+    """Many small pieces of changing size, then single tokens, step by step against append + flush."""
+    steps = [1, 2, 3, 5, 8, 13, 21, 34, 55, 1, 1, 89, 7]
+    case = Case(fmt, [0, 40], [sum(steps)] * 2, G=G, R=R, seed=8, extra=4).fill()
+    w, at = case.w, 0
+    for m in steps:
+        part = [slice(w.cu_seqlens[b] + n + at, w.cu_seqlens[b] + n + at + m) for b, n in enumerate(case.lens)]
+        pick = lambda a: np.ascontiguousarray(np.concatenate([a[p] for p in part]))
+        case.append(pick(w.k), pick(w.v), pick(case.classes), [m, m])
+        at += m
+        assert_state(case, oracle_of(case, [n + at for n in case.lens]))
+    rows = [w.cu_seqlens[b] + n + at for b, n in enumerate(case.lens)]
+    kn, vn, cls = (np.ascontiguousarray(a[rows]) for a in (w.k, w.v, case.classes))
+    if fmt == 6:
+        case.cache.append_flush_mixed(to_dev(kn), to_dev(vn), to_dev(cls))
+    else:
+        case.cache.append_flush(to_dev(kn), to_dev(vn))
+    assert_state(case, oracle_of(case, [n + at + 1 for n in case.lens]))
+
+
+def test_append_chunk_flushes_a_full_window():
+    """A window left full by append_token (no flush) is flushed by an empty chunk, as kvq_flush_group would."""
+    G, R = 32, 32
+    case = Case(4, [R + G - 1, 10], [1, 1], G=G, R=R, seed=11, extra=2).fill()
+    case.cache.append_token(to_dev(case.kn), to_dev(case.vn))
+    assert GpuState(case.cache).n_quant[:2].tolist() == [0, 0]
+    case.append(case.kn[:0], case.vn[:0], case.clsn[:0], [0, 0])
+    assert_state(case, oracle_of(case, [R + G, 11]))
+
+
+def test_append_chunk_dropped():
+    """A chunk past the capacity or longer than max_new, and a bad page, drop that sequence's chunk only."""
+    case = Case(4, [50, 60, 30], [14, 4, 40], G=32, R=0, seed=12)
+    cap = case.cache.shape.capacity                      # 96
+    case.fill()
+    before = GpuState(case.cache)
+    case.append(case.kn, case.vn, case.clsn, [14, 4, 40])
+    assert case.cache.error() == 0 and GpuState(case.cache).seq_len[:3].tolist() == [64, 64, 70]
+    rng = np.random.default_rng(1)
+    k = bits_of(rng.standard_normal((cap - 64 + 1 + 3 + 9, 2, 128)))
+    lens = [cap - 64 + 1, 3, 9]                          # the first does not fit
+    case.append(k, k, None, lens)
+    assert case.cache.error() == kvq.KVQ_DEVERR_APPEND_FULL
+    st = GpuState(case.cache)
+    assert st.seq_len[:3].tolist() == [64, 67, 79] and st.n_quant[:3].tolist() == [64, 64, 64]
+    case.cache.clear_error()
+    case.cache.append_chunk(to_dev(k[:13]), to_dev(k[:13]), cu_of([1, 3, 9]), 3)
+    assert case.cache.error() == kvq.KVQ_DEVERR_PREFILL_LEN
+    assert GpuState(case.cache).seq_len[:3].tolist() == [65, 70, 79]
+    assert before.cap == cap
+
+
+def test_append_chunk_bad_page():
+    case = Case(4, [40, 40], [40, 40], G=16, R=16, paged=True, seed=13).fill()
+    table = case.cache.region("page_table").view(torch.int32).view(2, -1)
+    keep = table.clone()
+    table[1, 3] = case.cache.shape.num_pages             # a page that the second chunk needs
+    case.append(case.kn, case.vn, None, [40, 40])
+    assert case.cache.error() == kvq.KVQ_DEVERR_PAGE_RANGE
+    st = GpuState(case.cache)
+    assert st.seq_len[:2].tolist() == [80, 40] and st.n_quant[:2].tolist() == [64, 16]
+    case.cache.clear_error()
+    table.copy_(keep)
+    case.append(case.kn[40:], case.vn[40:], None, [0, 40])
+    assert_state(case, oracle_of(case, [80, 80]))
+
+
+def test_append_chunk_leaves_other_bytes():
+    """8-bit tiles: the codes of tokens already held in a partly filled tile stay, and bytes of other units too."""
+    for fmt in (8, 16):
+        case = Case(fmt, [5, 37], [6, 3], seed=14).fill()
+        a = GpuState(case.cache)
+        case.append(case.kn, case.vn, None, [6, 3])
+        b = GpuState(case.cache)
+        for s, n in enumerate([5, 37]):
+            ua, ub = a.unit(s, 1, round_up(n, 16)), b.unit(s, 1, round_up(n, 16))
+            for name in ua:
+                assert np.array_equal(ua[name][:n], ub[name][:n]), (fmt, name)
+
+
+# ---------------------------------------------------------------------------
+# Read back
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt,G,R,paged", FORMATS)
+def test_read_tokens(fmt, G, R, paged):
+    lens = [0, 1, 15, 16, 17, R + G, 3 * G + R + 5, 700]
+    case = Case(fmt, lens, [0] * 8, G=G, R=R, paged=paged, seed=20 + fmt).fill()
+    st = GpuState(case.cache)
+    start = [0, 0, 3, 0, 16, 5, 2 * G + 7, 133]
+    take = [max(0, min(n - s, t)) for n, s, t in zip(lens, start, [0, 1, 100, 16, 1, R + G - 9, 3 * G, 555])]
+    for begin, length in ((None, lens), (torch.tensor(start, dtype=torch.int32, device="cuda"), take)):
+        rows = sum(length)
+        out = [torch.full((rows + 3, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        case.cache.read_tokens(begin, cu_of(length), max(length), *out)
+        torch.cuda.synchronize()
+        got = [o.float().cpu().numpy().astype(np.float64) for o in out]
+        at = 0
+        for b, n in enumerate(length):
+            s0 = 0 if begin is None else start[b]
+            for h in range(2):
+                for x, ref in zip(got, cached_rows(st, b, h)):
+                    r = ref[s0:s0 + n]
+                    # one rounding to fp32 and one to bf16
+                    assert np.all(np.abs(x[at:at + n, h] - r) <= np.abs(r) * (HALF_BF16 + 2.0 ** -20) + 1e-38), (b, h)
+            at += n
+        assert all(np.all(x[rows:] == 7.0) for x in got)     # rows behind the last range
+    only = torch.zeros(sum(lens), 2, 128, dtype=torch.bfloat16, device="cuda")
+    case.cache.read_tokens(None, cu_of(lens), max(lens), None, only)
+    full = torch.zeros_like(only)
+    case.cache.read_tokens(None, cu_of(lens), max(lens), torch.zeros_like(only), full)
+    assert torch.equal(only, full) and case.cache.error() == 0
+
+
+@pytest.mark.parametrize("fmt,G", [(4, 32), (2, 16)])
+def test_read_tokens_sparse_and_rope(fmt, G):
+    case = Case(fmt, [130, 64], [0, 0], G=G, R=16, sparse=True, seed=30).fill()
+    rope = Case(fmt, [130, 64], [0, 0], G=32, R=16, rope=10000.0, seed=30).fill()
+    for c in (case, rope):
+        out = [torch.empty(194, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        c.cache.read_tokens(None, c.cu, 130, *out)
+        torch.cuda.synchronize()
+        st = GpuState(c.cache)
+        for b, part in enumerate((slice(0, 130), slice(130, 194))):
+            for h in range(2):
+                for o, ref in zip(out, cached_rows(st, b, h)):
+                    x = o[part, h].float().cpu().numpy()
+                    assert np.all(np.abs(x - ref) <= np.abs(ref) * (HALF_BF16 + 2.0 ** -20) + 1e-38)
+
+
+def test_read_tokens_refused_ranges():
+    case = Case(4, [50, 60, 70], [0, 0, 0], G=16, R=16, paged=True, seed=31).fill()
+    out = [torch.full((100, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    start = torch.tensor([40, 0, 69], dtype=torch.int32, device="cuda")
+    case.cache.read_tokens(start, cu_of([11, 20, 1]), 20, *out)      # sequence 0 reads past its end
+    assert case.cache.error() == kvq.KVQ_DEVERR_PREFILL_LEN
+    assert torch.all(out[0][:11] == 7.0) and not torch.any(out[0][11:32] == 7.0) and torch.all(out[0][32:] == 7.0)
+    case.cache.clear_error()
+    table = case.cache.region("page_table").view(torch.int32).view(3, -1)
+    table[1, 1] = -1
+    out[1].fill_(7.0)
+    case.cache.read_tokens(None, cu_of([0, 40, 0]), 40, None, out[1])
+    assert case.cache.error() == kvq.KVQ_DEVERR_PAGE_RANGE
+    assert not torch.any(out[1][:16] == 7.0) and torch.all(out[1][16:32] == 7.0) and not torch.any(out[1][32:40] == 7.0)
+
+
+# ---------------------------------------------------------------------------
+# Chunk attention
+# ---------------------------------------------------------------------------
+
+LENS = [0, 1, 15, 33, 64, 130, 700]
+NEW = [5, 1, 0, 40, 129, 3, 70]
+
+
+@pytest.mark.parametrize("fmt,G,R,paged", FORMATS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 4), (1, 0), (129, 70)])
+def test_chunk_attention(fmt, G, R, paged, window, sinks):
+    case = Case(fmt, LENS, NEW, G=G, R=R, paged=paged, seed=40 + fmt + G).fill()
+    case.check(case.attend(window=window, sinks=sinks), window, sinks)
+    assert case.cache.error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (10, 2), (7, 1), (16, 2), (12, 6)])
+def test_chunk_attention_heads(hq, hkv):
+    case = Case(4, [200, 0, 47], [37, 61, 2], hq=hq, hkv=hkv, seed=50 + hq).fill()
+    case.check(case.attend())
+
+
+@pytest.mark.parametrize("fmt", [2, 4, 6, 8, 16])
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 40])
+def test_chunk_attention_splits(fmt, splits):
+    case = Case(fmt, [1300, 5, 400], [3, 1, 9], seed=60 + fmt).fill()
+    case.check(case.attend(splits=splits))
+    case.check(case.attend(splits=splits, window=300, sinks=7), 300, 7)
+
+
+@pytest.mark.parametrize("n,m", [(1, 1), (127, 1), (128, 1), (129, 255), (2049, 300), (0, 513)])
+def test_chunk_attention_edges(n, m):
+    for fmt, R in ((4, 0), (4, 128), (16, 0)):
+        case = Case(fmt, [n], [m], hq=4, hkv=1, R=R, seed=70).fill()
+        case.check(case.attend())
+        case.check(case.attend(window=64, sinks=130), 64, 130)
+
+
+@pytest.mark.parametrize("fmt,G", [(4, 32), (2, 16)])
+def test_chunk_attention_sparse(fmt, G):
+    case = Case(fmt, [130, 0, 64], [33, 5, 1], G=G, R=16, sparse=True, seed=80, k_outlier=20.0).fill()
+    case.check(case.attend())
+    case.check(case.attend(window=40, sinks=3), 40, 3)
+
+
+@pytest.mark.parametrize("fmt", [2, 4])
+def test_chunk_attention_rope(fmt):
+    case = Case(fmt, [130, 0, 700], [33, 5, 1], R=16, rope=10000.0, seed=81).fill()
+    case.check(case.attend(), rope=10000.0)
+    case.check(case.attend(window=40, sinks=3), 40, 3, rope=10000.0)
+
+
+def test_chunk_attention_bad_page():
+    case = Case(4, [200, 90], [20, 7], G=16, R=16, paged=True, seed=82).fill()
+    st = GpuState(case.cache)
+    table = case.cache.region("page_table").view(torch.int32).view(2, -1)
+    keep = table.clone()
+    table[0, 3] = -1
+    table[1, 0] = case.cache.shape.num_pages
+    out = case.attend()
+    assert case.cache.error() == kvq.KVQ_DEVERR_PAGE_RANGE
+    table.copy_(keep)
+    case.check(out, skip_pages=[(0, 3), (1, 0)])
+    assert st.seq_len[:2].tolist() == [200, 90]
+
+
+def test_chunk_attention_skips_and_leaves_rows():
+    """A chunk longer than max_new and rows behind the last chunk stay as they were."""
+    case = Case(4, [100, 50], [9, 4], seed=83).fill()
+    out = torch.full((16, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(16, 8, 128, dtype=torch.bfloat16, device="cuda")
+    q[:13] = to_dev(case.q).view(torch.bfloat16)
+    k, v = (torch.full((16, 2, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[:13], v[:13] = to_dev(case.kn).view(torch.bfloat16), to_dev(case.vn).view(torch.bfloat16)
+    n = case.cache.chunk_workspace_bytes(0, 16, 9, 100)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    case.cache.chunk_attention(q, k, v, case.cu_new, 9, out, SCALE, ws, 0, 100)
+    torch.cuda.synchronize()
+    assert torch.all(out[13:] == 7.0)
+    case.check(out[:13].float().cpu().numpy().astype(np.float64))
+    out.fill_(7.0)
+    case.cache.chunk_attention(q, k, v, case.cu_new, 8, out, SCALE, ws, 0, 100)      # the first chunk has 9
+    assert case.cache.error() == kvq.KVQ_DEVERR_PREFILL_LEN
+    assert torch.all(out[:9] == 7.0) and not torch.any(out[9:13] == 7.0)
+
+
+def test_prompt_in_pieces_then_decode():
+    """The operators as a server uses them: pieces of a prompt attend and are appended, then a decode step; the cache ends
+    up as one prefill of the whole prompt leaves it, and the last piece's output is that of the reference."""
+    pieces = [[100, 3], [64, 0], [33, 50]]
+    case = Case(4, [0, 0], [197, 53], seed=90)
+    w = case.w
+    at = [0, 0]
+    for piece in pieces:
+        part = [slice(w.cu_seqlens[b] + at[b], w.cu_seqlens[b] + at[b] + m) for b, m in enumerate(piece)]
+        pick = lambda a: np.ascontiguousarray(np.concatenate([a[p] for p in part]))
+        step = Case.__new__(Case)
+        step.__dict__.update(case.__dict__)
+        step.lens, step.new, step.kn, step.vn = list(at), piece, pick(w.k), pick(w.v)
+        step.q = case.q[:sum(piece)]
+        step.cu_new = cu_of(piece)
+        step.check(step.attend())
+        case.append(step.kn, step.vn, None, piece)
+        at = [a + m for a, m in zip(at, piece)]
+    assert_state(case, oracle_of(case, at))
+    out = torch.empty(2, 8, 128, device="cuda")
+    ws = torch.empty(case.cache.workspace_bytes(0, max(at)), dtype=torch.uint8, device="cuda")
+    case.cache.decode_attention(to_dev(w.q), out, SCALE, ws, 0, max(at))
+    st = GpuState(case.cache)
+    for b in range(2):
+        for h in range(8):
+            k, v = cached_rows(st, b, h // 4)
+            ref, _, tol = attend(bf16(w.q[b, h])[None], k, v, [at[b] - 1], SCALE)
+            assert np.all(np.abs(out[b, h].cpu().numpy() - ref[0]) <= tol[0])
+
+
+def test_chunk_captured_and_replayed():
+    """Append, read and chunk attention in a CUDA graph on a side stream, replayed on new inputs."""
+    case = Case(4, [300, 7], [20, 4], seed=91, extra=60).fill()
+    c, w = case.cache, case.w
+    q, k, v = (to_dev(a).view(torch.bfloat16).clone() for a in (case.q, case.kn, case.vn))
+    out = torch.empty_like(q)
+    n = c.chunk_workspace_bytes(0, 24, 20, 360)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        c.chunk_attention(q, k, v, case.cu_new, 20, out, SCALE, ws, 0, 360)
+        c.append_chunk(k, v, case.cu_new, 20)
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                      # warm-up: the first piece
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    lens = [320, 11]
+    for i in range(2):                              # the same piece again and again, behind itself
+        graph.replay()
+        torch.cuda.synchronize()
+        lens = [n + m for n, m in zip(lens, case.new)]
+        assert GpuState(c).seq_len[:2].tolist() == lens
+        eager = torch.empty_like(out)
+        # what the replay saw: the state before its append
+        c.seq_len()[:2].copy_(torch.tensor([n - m for n, m in zip(lens, case.new)], dtype=torch.int32))
+        st = GpuState(c)
+        if all(st.n_quant <= st.seq_len):
+            c.chunk_attention(q, k, v, case.cu_new, 20, eager, SCALE, ws, 0, 360)
+        c.seq_len()[:2].copy_(torch.tensor(lens, dtype=torch.int32))
+    assert c.error() == 0
+
+
+@pytest.mark.parametrize("bad", ["inf", "nan"])
+def test_later_tokens_do_not_reach_earlier_rows(bad):
+    """An infinity or NaN in a new token is hidden from the rows before it."""
+    case = Case(4, [70], [40], seed=92).fill()
+    clean = case.attend()
+    kn, vn = case.kn.copy(), case.vn.copy()
+    kn[25], vn[25] = (0x7F80, 0x7F80) if bad == "inf" else (0x7FC0, 0x7FC0)
+    case.kn, case.vn = kn, vn
+    out = case.attend()
+    assert np.array_equal(out[:25], clean[:25])
+    assert not np.any(np.isfinite(out[25:]))
