@@ -306,11 +306,52 @@ kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q_bf16, const
   A.v = (const uint16_t*)v_new_bf16;
   A.cu = cu_seqlens_dev;
   A.out = (uint16_t*)out_bf16;
+  A.out32 = A.lse = nullptr;
   A.ws_o = (float*)workspace;
   A.ws_ml = nullptr;
   A.scale_log2 = softmax_scale * 1.4426950408889634f;
   A.rows = total_new;
   A.max_new = max_new;
+  A.window = window;
+  A.sinks = sinks;
+  A.splits = splits;
+  return from_cuda(launch_chunk_attention(A, (cudaStream_t)stream));
+}
+
+// Split count of a windowed decode call (0 = the library's choice), or 0 if an argument is out of range.
+static int window_splits(const kvq_shape& s, int32_t num_splits, int32_t max_len, int32_t window, int32_t sinks) {
+  return chunk_splits(s, num_splits, s.batch, 1, max_len, window, sinks);
+}
+
+size_t kvq_window_workspace_bytes(const kvq_cache* cache, int32_t num_splits, int32_t max_len, int32_t window,
+                                  int32_t sinks) {
+  if (!cache || check_shape(&cache->shape) != KVQ_OK) return 0;
+  const int splits = window_splits(cache->shape, num_splits, max_len, window, sinks);
+  return splits ? chunk_workspace_bytes(cache->shape, splits, cache->shape.batch) : 0;
+}
+
+kvq_status kvq_decode_attention_window(const kvq_cache* cache, const void* q_bf16, float* out, float* lse,
+                                       float softmax_scale, int32_t window, int32_t sinks, void* workspace,
+                                       size_t ws_bytes, int32_t num_splits, int32_t max_len, kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!q_bf16 || !out || !(softmax_scale == softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  const kvq_shape& s = cache->shape;
+  const int splits = window_splits(s, num_splits, max_len, window, sinks);
+  if (!splits) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  const size_t need = chunk_workspace_bytes(s, splits, s.batch);
+  if (need > 0 && !workspace) return KVQ_ERR_INVALID_ARG;
+  if (ws_bytes < need) return KVQ_ERR_WORKSPACE;
+  ChunkAttnArgs A = {};
+  A.c = *cache;
+  A.q = (const uint16_t*)q_bf16;
+  A.out32 = out;
+  A.lse = lse;
+  A.ws_o = (float*)workspace;
+  A.scale_log2 = softmax_scale * 1.4426950408889634f;
+  A.rows = s.batch;
+  A.max_new = 1;
   A.window = window;
   A.sinks = sinks;
   A.splits = splits;

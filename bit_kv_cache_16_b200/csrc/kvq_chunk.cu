@@ -50,9 +50,8 @@ __global__ void __launch_bounds__(128) chunk_general_kernel(ChunkAttnArgs A) {
     sm.q[r][2 * w + 1] = bf16_hi(x);
   }
   const int row = tid >> 2, l = tid & 3;
-  const int p_row = sq.n + min(r0 + row, rows - 1) / gq;               // this row's position
-  const TileRange range(sq.n + r0 / gq, sq.n + (min(r0 + kGenRows, rows) - 1) / gq, A.window, A.sinks, kGenKeys);
-  const int total = sq.n + sq.m;
+  const int p_row = sq.p0 + min(r0 + row, rows - 1) / gq;               // this row's position
+  const TileRange range(sq.p0 + r0 / gq, sq.p0 + (min(r0 + kGenRows, rows) - 1) / gq, A.window, A.sinks, kGenKeys);
   const int Ws = window_slots(s);
   float m = -INFINITY, sum = 0.f, o[32];
 #pragma unroll
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(128) chunk_general_kernel(ChunkAttnArgs A) {
         if (t < sq.n)
           w = *reinterpret_cast<const uint4*>((const uint16_t*)(key ? c.k_res : c.v_res) +
                                               Addr::ring_row(s, b, kv, t % Ws) + ch);
-        else if (t < total)
+        else if (t < sq.total)
           w = *reinterpret_cast<const uint4*>((key ? A.k : A.v) +
                                               ((size_t)(sq.t0 + t - sq.n) * s.num_kv_heads + kv) * kHeadDim + ch);
         const float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
@@ -158,6 +157,15 @@ __global__ void __launch_bounds__(128) chunk_general_kernel(ChunkAttnArgs A) {
   if (r0 + row >= rows) return;
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
   const int R = r0 + row;
+  if (A.out32) {
+    const size_t at = (size_t)(sq.t0 + R / gq) * s.num_q_heads + kv * gq + R % gq;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(A.out32 + at * kHeadDim + 4 * (l + 4 * i)) =
+          make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+    if (A.lse && l == 0) A.lse[at] = (m + log2f(sum)) * 0.69314718055994531f;
+    return;
+  }
   uint16_t* dst = A.out + ((size_t)(sq.t0 + R / gq) * s.num_q_heads + kv * gq + R % gq) * kHeadDim;
 #pragma unroll
   for (int i = 0; i < 8; ++i)

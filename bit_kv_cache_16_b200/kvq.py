@@ -42,6 +42,7 @@ REGIONS = ["k_codes", "k_meta", "v_codes", "v_meta", "k_res", "v_res", "seq_len"
 EXPORTED = ["kvq_buffer_bytes", "kvq_quantize_prefill", "kvq_append_token", "kvq_flush_group", "kvq_append_flush",
             "kvq_quantize_prefill_mixed", "kvq_append_token_mixed", "kvq_append_flush_mixed",
             "kvq_append_chunk", "kvq_read_tokens", "kvq_chunk_attention", "kvq_chunk_workspace_bytes",
+            "kvq_decode_attention_window", "kvq_window_workspace_bytes",
             "kvq_decode_attention", "kvq_decode_attention_lse", "kvq_merge_partials",
             "kvq_decode_attention_noalloc", "kvq_decode_workspace_bytes", "kvq_decode_default_splits",
             "kvq_read_error", "kvq_status_string", "kvq_version"]
@@ -92,6 +93,8 @@ def load(path: Optional[str] = None):
         "kvq_read_tokens": (i32, [pc, vp, vp, i32, vp, vp, vp]),
         "kvq_chunk_attention": (i32, [pc, vp, vp, vp, vp, i32, i32, f32, i32, i32, vp, vp, sz, i32, i32, vp]),
         "kvq_chunk_workspace_bytes": (sz, [pc, i32, i32, i32, i32, i32, i32]),
+        "kvq_decode_attention_window": (i32, [pc, vp, vp, vp, f32, i32, i32, vp, sz, i32, i32, vp]),
+        "kvq_window_workspace_bytes": (sz, [pc, i32, i32, i32, i32]),
         "kvq_decode_attention": (i32, [pc, vp, vp, f32, vp, sz, i32, i32, vp]),
         "kvq_decode_attention_lse": (i32, [pc, vp, vp, vp, f32, vp, sz, i32, i32, vp]),
         "kvq_merge_partials": (i32, [vp, vp, i32, ctypes.c_int64, vp, vp, vp]),
@@ -217,6 +220,20 @@ def kvq_chunk_workspace_bytes(cache: KvqCache, num_splits: int, total_new: int, 
                               window: int = 0, sinks: int = 0) -> int:
     return int(load().kvq_chunk_workspace_bytes(ctypes.byref(cache), int(num_splits), int(total_new), int(max_new),
                                                 int(max_len), int(window), int(sinks)))
+
+
+def kvq_decode_attention_window(cache: KvqCache, q, out, lse, softmax_scale: float, window: int, sinks: int,
+                                workspace, ws_bytes: int, num_splits: int, max_len: int, stream=None):
+    """Decode over the last `window` tokens and the first `sinks` (lse None: not written)."""
+    _check("kvq_decode_attention_window",
+           load().kvq_decode_attention_window(ctypes.byref(cache), _ptr(q), _ptr(out), _ptr(lse),
+                                              float(softmax_scale), int(window), int(sinks), _ptr(workspace),
+                                              int(ws_bytes), int(num_splits), int(max_len), _stream(stream)))
+
+
+def kvq_window_workspace_bytes(cache: KvqCache, num_splits: int, max_len: int, window: int, sinks: int = 0) -> int:
+    return int(load().kvq_window_workspace_bytes(ctypes.byref(cache), int(num_splits), int(max_len), int(window),
+                                                 int(sinks)))
 
 
 def kvq_decode_workspace_bytes(cache: KvqCache, num_splits: int, max_len: int) -> int:
@@ -353,6 +370,13 @@ class Cache:
             raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape),
                                                          tuple("*" if e is None else e for e in shape)))
 
+    def _bytes_of(self, workspace) -> int:
+        """Bytes of a workspace tensor (contiguous, on the cache's device) or 0 for None."""
+        if workspace is None:
+            return 0
+        self._need("workspace", workspace, tuple(workspace.shape), workspace.element_size())
+        return workspace.numel() * workspace.element_size()
+
     def _guard(self, stream):
         """(a context in which the cache's device is current, the stream to use)."""
         dev = self.buffers["seq_len"].device
@@ -405,11 +429,28 @@ class Cache:
         self._need("v_new", v_new, (rows, s.num_kv_heads, 128), 2)
         self._need("out", out, (rows, s.num_q_heads, 128), 2)
         self._need("cu_seqlens", cu_seqlens, (s.batch + 1,), 4)
-        n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        n = self._bytes_of(workspace)
         ctx, stream = self._guard(stream)
         with ctx:
             kvq_chunk_attention(self.desc, q, k_new, v_new, cu_seqlens, rows, max_new, softmax_scale, window, sinks,
                                 out, workspace, n, num_splits, max_len, stream)
+
+    def window_workspace_bytes(self, num_splits: int, max_len: int, window: int, sinks: int = 0) -> int:
+        return kvq_window_workspace_bytes(self.desc, num_splits, max_len, window, sinks)
+
+    def decode_attention_window(self, q, out, softmax_scale: float, window: int, sinks: int, workspace,
+                                num_splits: int, max_len: int, lse=None, stream=None):
+        """out float [B, H_q, 128]: one query per sequence over its last `window` tokens and its first `sinks`."""
+        s = self.shape
+        self._need("q", q, (s.batch, s.num_q_heads, 128), 2)
+        self._need("out", out, (s.batch, s.num_q_heads, 128), 4)
+        if lse is not None:
+            self._need("lse", lse, (s.batch, s.num_q_heads), 4)
+        n = self._bytes_of(workspace)
+        ctx, stream = self._guard(stream)
+        with ctx:
+            kvq_decode_attention_window(self.desc, q, out, lse, softmax_scale, window, sinks, workspace, n, num_splits,
+                                        max_len, stream)
 
     def workspace_bytes(self, num_splits: int, max_len: int) -> int:
         return kvq_decode_workspace_bytes(self.desc, num_splits, max_len)

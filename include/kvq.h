@@ -477,6 +477,32 @@ kvq_status kvq_chunk_attention(const kvq_cache *cache, const void *q_bf16, const
 size_t kvq_chunk_workspace_bytes(const kvq_cache *cache, int32_t num_splits, int32_t total_new, int32_t max_new,
                                  int32_t max_len, int32_t window, int32_t sinks);
 
+/*
+ * kvq_decode_attention_lse over part of the cache only: the query of sequence
+ * b stands at its last token, p = seq_len[b] - 1, and sees the last `window`
+ * tokens (t > p - window) and the first `sinks` tokens (t < sinks); window 0 =
+ * every token.  Only the visible tokens' tiles are read.
+ *  q_bf16:     bf16 [B][H_q][D]
+ *  out:        float [B][H_q][D]
+ *  lse:        float [B][H_q], or NULL
+ *  window, sinks: >= 0
+ *  workspace:  kvq_window_workspace_bytes(cache, num_splits, max_len, window,
+ *              sinks) bytes, as kvq_chunk_attention's; may be NULL if that is 0.
+ *  num_splits: >= 1: the visible keys are cut into that many ranges; 0 = the
+ *              library's choice.
+ *  max_len:    an upper bound of seq_len over the batch (for that choice).
+ * A sequence without tokens gets out = 0 and lse = -inf; one with an
+ * inconsistent state (KVQ_DEVERR_STATE) is skipped, its rows left as they
+ * were; a page whose id is out of range is left out (KVQ_DEVERR_PAGE_RANGE).
+ */
+kvq_status kvq_decode_attention_window(const kvq_cache *cache, const void *q_bf16, float *out, float *lse,
+                                       float softmax_scale, int32_t window, int32_t sinks, void *workspace,
+                                       size_t ws_bytes, int32_t num_splits, int32_t max_len, kvq_stream_t stream);
+
+/* Workspace bytes kvq_decode_attention_window needs (0 for bad arguments too). */
+size_t kvq_window_workspace_bytes(const kvq_cache *cache, int32_t num_splits, int32_t max_len, int32_t window,
+                                  int32_t sinks);
+
 /* Workspace bytes kvq_decode_attention needs for this split count (0 = the
  * library's choice for max_len). */
 size_t kvq_decode_workspace_bytes(const kvq_cache *cache, int32_t num_splits, int32_t max_len);

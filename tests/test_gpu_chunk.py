@@ -5,7 +5,7 @@ import torch
 
 from bit_kv_cache_16_b200 import kvq, synth
 
-from chunk_ref import HALF_BF16, attend, bf16, cached_rows, rotate
+from chunk_ref import HALF_BF16, HALF_FP16, attend, bf16, cached_rows, rotate
 from gpu_harness import (assert_fp8_state, assert_int8_state, assert_unit_state, make_gpu_cache, oracle_cache, round_up,
                          to_dev)
 from layout import GpuState
@@ -466,3 +466,113 @@ def test_later_tokens_do_not_reach_earlier_rows(bad):
     out = case.attend()
     assert np.array_equal(out[:25], clean[:25])
     assert not np.any(np.isfinite(out[25:]))
+
+
+# ---------------------------------------------------------------------------
+# Windowed decode
+# ---------------------------------------------------------------------------
+
+def decode_window(case, window, sinks, splits=0, max_len=None):
+    c, w = case.cache, case.w
+    out = torch.full((w.batch, w.num_q_heads, 128), float("nan"), device="cuda")
+    lse = torch.full((w.batch, w.num_q_heads), float("nan"), device="cuda")
+    max_len = max(case.lens) if max_len is None else max_len
+    n = c.window_workspace_bytes(splits, max_len, window, sinks)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    c.decode_attention_window(to_dev(w.q), out, SCALE, window, sinks, ws, splits, max_len, lse=lse)
+    torch.cuda.synchronize()
+    return out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+
+
+def check_decode(case, got, window, sinks, rope=0.0, skip_pages=()):
+    out, lse = got
+    st = GpuState(case.cache)
+    gq = case.w.num_q_heads // case.w.num_kv_heads
+    for b, n in enumerate(case.lens):
+        present = np.ones(n, bool)
+        for bb, page in skip_pages:
+            if bb == b:
+                present[16 * page:16 * page + 16] = False
+        for h in range(case.w.num_q_heads):
+            if n == 0:
+                assert np.all(out[b, h] == 0) and lse[b, h] == -np.inf
+                continue
+            k, v = cached_rows(st, b, h // gq, rope > 0, rope)
+            q = bf16(case.w.q[b, h])[None]
+            ref, ref_lse, tol = attend(q, k, v, [n - 1], SCALE, window, sinks, present)
+            err = np.abs(out[b, h] - ref[0])
+            assert np.all(err <= tol[0]), (b, h, float(np.nanmax(err / tol[0])), int(np.isnan(out[b, h]).sum()))
+            # a score is off by at most d (attend's comment), and so is the log of their exponentials' sum
+            d = SCALE * (np.abs(q) @ np.abs(k).T).max() * (HALF_FP16 + 2.0 ** -17) + 2.0 ** -17
+            assert abs(lse[b, h] - ref_lse[0]) <= d, (b, h, lse[b, h], ref_lse[0])
+
+
+@pytest.mark.parametrize("fmt,G,R,paged", FORMATS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (50, 4), (129, 70), (10000, 3)])
+def test_window_decode(fmt, G, R, paged, window, sinks):
+    case = Case(fmt, [0, 1, 15, 33, 64, 130, 1100], [0] * 7, G=G, R=R, paged=paged, seed=100 + fmt + G).fill()
+    for splits in (0, 1, 3):
+        check_decode(case, decode_window(case, window, sinks, splits), window, sinks)
+    assert case.cache.error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (10, 2), (8, 1), (12, 6)])
+def test_window_decode_heads(hq, hkv):
+    case = Case(2, [300, 0, 47], [0] * 3, hq=hq, hkv=hkv, seed=110).fill()
+    check_decode(case, decode_window(case, 100, 5), 100, 5)
+
+
+def test_window_decode_sparse_and_rope():
+    for kw in (dict(sparse=True, G=16, k_outlier=20.0), dict(rope=10000.0)):
+        case = Case(4, [300, 1, 47], [0] * 3, R=16, seed=111, **kw).fill()
+        check_decode(case, decode_window(case, 100, 5), 100, 5, rope=kw.get("rope", 0.0))
+
+
+def test_window_decode_bad_page_and_state():
+    case = Case(4, [200, 90, 40], [0] * 3, G=16, R=16, paged=True, seed=112).fill()
+    table = case.cache.region("page_table").view(torch.int32).view(3, -1)
+    keep = table.clone()
+    table[0, 3], table[1, 0] = -1, case.cache.shape.num_pages
+    got = decode_window(case, 170, 20)
+    assert case.cache.error() == kvq.KVQ_DEVERR_PAGE_RANGE
+    table.copy_(keep)
+    check_decode(case, got, 170, 20, skip_pages=[(0, 3), (1, 0)])
+    case.cache.clear_error()
+    case.cache.n_quant()[1] = 7
+    out, _ = decode_window(case, 0, 0)
+    assert case.cache.error() == kvq.KVQ_DEVERR_STATE
+    assert np.all(np.isnan(out[1])) and np.all(np.isfinite(out[0])) and np.all(np.isfinite(out[2]))
+
+
+@pytest.mark.parametrize("fmt", [2, 4, 6, 8, 16])
+def test_window_decode_equals_full_decode(fmt):
+    """A window over everything gives what the unwindowed decode gives, within the roundings of both."""
+    case = Case(fmt, [700, 90, 0], [0] * 3, seed=113).fill()
+    c, w = case.cache, case.w
+    out = torch.empty(3, 8, 128, device="cuda")
+    ws = torch.empty(c.workspace_bytes(0, 700), dtype=torch.uint8, device="cuda")
+    c.decode_attention(to_dev(w.q), out, SCALE, ws, 0, 700)
+    got, _ = decode_window(case, 700, 0)
+    st = GpuState(c)
+    for b, n in enumerate(case.lens):
+        for h in range(8):
+            k, v = cached_rows(st, b, h // 4)
+            if n:
+                tol = attend(bf16(w.q[b, h])[None], k, v, [n - 1], SCALE)[2][0]
+                assert np.all(np.abs(got[b, h] - out[b, h].cpu().numpy()) <= 2 * tol)
+
+
+def test_hidden_values_do_not_reach_the_row():
+    """NaN and infinities in tokens outside the window (quantized ones and window ones) change nothing."""
+    for fmt, R in ((4, 64), (16, 0)):
+        case = Case(fmt, [200], [0], R=R, seed=114).fill()
+        clean = decode_window(case, 20, 3)
+        kq, vq = case.k.copy(), case.v.copy()
+        for t, x in ((45, 0x7FC0), (70, 0x7F80), (150, 0x7FC0), (178, 0x7F80)):
+            kq[t], vq[t] = x, x
+        vq[10] = 0x7FC0                             # in the sinks' value tile (keys share their group's scale)
+        case.cache.reset()
+        case.append(kq, vq, None, [200])
+        got = decode_window(case, 20, 3)
+        for a, b in zip(clean, got):
+            assert np.array_equal(a, b), fmt
