@@ -1,202 +1,762 @@
-// kvq_chunk_attention, general form: a chunk of new tokens attends to the
-// packed cache and causally to itself, in fp32 on the CUDA cores.
-#include "kvq_chunk.cuh"
-#include "kvq_rows.cuh"
+// kvq_chunk_attention and kvq_decode_attention_window: query rows against the
+// packed cache (and causally against the chunk's own tokens) on the tensor
+// cores.
+//
+// Per (sequence, kv head) the query rows of all gq heads and new tokens form
+// one matrix (row R = head R % gq of token R / gq).  For each tile of 128
+// tokens: S = Q K^T (128 rows x 128 keys, fp16 operands, fp32 in TMEM), the
+// online softmax with one thread per row, P = fp16 back into TMEM, O += P V
+// with O in TMEM.  Packed tokens become fp16 operands once per CTA and tile
+// (kvq_tiles.cuh); fp16 holds every code exactly and a dequantized number to
+// 2^-11, eight times finer than bf16, and powers of two are taken out of raw
+// rows that would not fit.
+#include "kvq_tiles.cuh"
 
 namespace kvq {
 
-constexpr int kGenRows = 32;                 // query rows per CTA
-constexpr int kGenKeys = 32;                 // keys per step: two 16-token tiles
-constexpr int kGenPad = kHeadDim + 4;        // floats per row (16-byte aligned, rows in different banks)
+constexpr int kRows = 128;                   // query rows per stream: one TMEM lane and one softmax thread each
+constexpr int kProducerWarp = 8;             // warps 0-3 and 4-7: softmax of streams 0 and 1; 8-11: producers
+constexpr int kMmaWarp = 12;
+constexpr int kChunkThreads = 32 * (kMmaWarp + 1);
+constexpr int kStages = 2;                   // key tiles and value tiles in flight
+constexpr int kInfos = 4;                    // tile descriptions in flight
+constexpr float kSlack = 8.f;                // the reference maximum may lag by 2^8 (P stays below fp16's 65504)
+constexpr unsigned long long kWaitNs = 2000000000ull;
 
-struct GenSmem {
-  float q[kGenRows][kGenPad];
-  float k[kGenKeys][kGenPad];
-  float v[kGenKeys][kGenPad];
-  float p[kGenRows][kGenKeys + 1];
+struct ChunkCtrl {
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_ready[2], o_done[2], drained;
+  uint32_t tmem;
+  int abort;
+  TileInfo info[kInfos];
+  float qmul[2 * kRows];                     // 2^e of each query row
+  float ml[kRows][2];                        // paired streams: (m, l) of stream 1
   double freq[kHeadDim / 2];                 // RoPE pair frequencies
-  int skipped[2];                            // the step's tiles whose page id is bad
 };
 
-// Grid (row blocks, H_kv, B), 128 threads.  Row r of a unit is head r % gq of
-// new token r / gq.  Each step brings 32 keys and values as fp32 into shared
-// memory (warps 0, 1 keys, warps 2, 3 values; one 16-token tile each): from the
-// packed tiles, the window ring or the chunk, keys stored before RoPE rotated
-// by their position.  Four threads share a row: scores of every fourth key,
-// then 32 channels each of the value sum.  Softmax online, everything in fp32.
-// Bound by the fp32 rate of the two products.
-template <int FMT>
-__global__ void __launch_bounds__(128) chunk_general_kernel(ChunkAttnArgs A) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  GenSmem& sm = *reinterpret_cast<GenSmem*>(raw);
-  const kvq_cache& c = A.c;
-  const kvq_shape& s = c.shape;
-  const int kv = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gq = s.num_q_heads / s.num_kv_heads;
-  const ChunkSeq sq = chunk_seq(A, b);
-  if (sq.err && blockIdx.x == 0 && kv == 0 && tid == 0) atomicOr(c.err_word, sq.err);
-  const int r0 = blockIdx.x * kGenRows, rows = sq.m * gq;
-  if (r0 >= rows) return;
-  const bool rope = s.rope_theta > 0.f;
-  if (rope && tid < kHeadDim / 2)
-    sm.freq[tid] = pow((double)s.rope_theta, -2.0 * (double)tid / (double)kHeadDim);
-  for (int e = tid; e < kGenRows * kHeadDim / 2; e += 128) {
-    const int r = e / (kHeadDim / 2), w = e % (kHeadDim / 2), R = r0 + r;
-    uint32_t x = 0u;
-    if (R < rows)
-      x = reinterpret_cast<const uint32_t*>(
-          A.q + ((size_t)(sq.t0 + R / gq) * s.num_q_heads + kv * gq + R % gq) * kHeadDim)[w];
-    sm.q[r][2 * w] = bf16_lo(x);
-    sm.q[r][2 * w + 1] = bf16_hi(x);
-  }
-  const int row = tid >> 2, l = tid & 3;
-  const int p_row = sq.p0 + min(r0 + row, rows - 1) / gq;               // this row's position
-  const TileRange range(sq.p0 + r0 / gq, sq.p0 + (min(r0 + kGenRows, rows) - 1) / gq, A.window, A.sinks, kGenKeys);
-  const int Ws = window_slots(s);
-  float m = -INFINITY, sum = 0.f, o[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) o[i] = 0.f;
-
-  for (int it = 0; it < range.count; ++it) {
-    const int t0 = range.tile(it) * kGenKeys;
-    __syncthreads();                         // the last step's tiles are used up
-    {
-      const bool key = warp < 2;
-      const int base = 16 * (warp & 1), tile = t0 / kTile + (warp & 1);
-      float(*dst)[kGenPad] = key ? sm.k : sm.v;
-      auto put = [&](int r, int ch, const float (&x)[8]) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i];
-        if (key && rope) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float cs, sn;
-            rope_cos_sin(tile * kTile + r, sm.freq[ch / 2 + i], cs, sn);
-            y[2 * i] = x[2 * i] * cs - x[2 * i + 1] * sn;
-            y[2 * i + 1] = x[2 * i] * sn + x[2 * i + 1] * cs;
-          }
-        }
-        float4* d4 = reinterpret_cast<float4*>(&dst[base + r][ch]);
-        d4[0] = make_float4(y[0], y[1], y[2], y[3]);
-        d4[1] = make_float4(y[4], y[5], y[6], y[7]);
-      };
-      const int quant = min(max(sq.nq - tile * kTile, 0), kTile);      // the tile's quantized rows come first
-      bool ok = true;
-      if (quant > 0) {
-        TileSrc d;
-        ok = tile_src<FMT>(c, b, kv, tile, d);
-        if (ok) {
-          if (key) key_rows<FMT>(d, 0, quant, put);
-          else value_rows<FMT>(d, 0, quant, put);
-        } else if (lane == 0 && key) atomicOr(c.err_word, KVQ_DEVERR_PAGE_RANGE);
-      }
-      if (lane == 0 && key) sm.skipped[warp] = ok ? 0 : 1;
-      for (int r = quant + (lane >> 4); r < kTile; r += 2) {
-        const int t = tile * kTile + r, ch = 8 * (lane & 15);
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (t < sq.n)
-          w = *reinterpret_cast<const uint4*>((const uint16_t*)(key ? c.k_res : c.v_res) +
-                                              Addr::ring_row(s, b, kv, t % Ws) + ch);
-        else if (t < sq.total)
-          w = *reinterpret_cast<const uint4*>((key ? A.k : A.v) +
-                                              ((size_t)(sq.t0 + t - sq.n) * s.num_kv_heads + kv) * kHeadDim + ch);
-        const float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
-                            bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-        put(r, ch, x);
-      }
-    }
-    __syncthreads();
-    float sc[8], top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int j = l + 4 * i, t = t0 + j;
-      sc[i] = -INFINITY;
-      if (!key_visible(t, p_row, A.window, A.sinks) || (t < sq.nq && sm.skipped[j / kTile])) continue;
-      float d = 0.f;
-      const float4* qr = reinterpret_cast<const float4*>(sm.q[row]);
-      const float4* kr = reinterpret_cast<const float4*>(sm.k[j]);
-#pragma unroll 8
-      for (int e = 0; e < kHeadDim / 4; ++e) {
-        const float4 x = qr[e], y = kr[e];
-        d = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, d))));
-      }
-      sc[i] = d * A.scale_log2;
-      top = fmaxf(top, sc[i]);
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ref);            // 0 while m is -inf
-    sum *= f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] *= f;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float e = ex2(sc[i] - ref);
-      sum += e;
-      sm.p[row][l + 4 * i] = e;
-    }
-    __syncwarp();
-#pragma unroll 1
-    for (int j = 0; j < kGenKeys; ++j) {
-      const float p = sm.p[row][j];
-      if (p == 0.f) continue;                // hidden keys' values may be anything, infinities too
-      const float4* vr = reinterpret_cast<const float4*>(sm.v[j]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 x = vr[l + 4 * i];
-        o[4 * i] = fmaf(p, x.x, o[4 * i]); o[4 * i + 1] = fmaf(p, x.y, o[4 * i + 1]);
-        o[4 * i + 2] = fmaf(p, x.z, o[4 * i + 2]); o[4 * i + 3] = fmaf(p, x.w, o[4 * i + 3]);
-      }
-    }
-  }
-  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  if (r0 + row >= rows) return;
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  const int R = r0 + row;
-  if (A.out32) {
-    const size_t at = (size_t)(sq.t0 + R / gq) * s.num_q_heads + kv * gq + R % gq;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<float4*>(A.out32 + at * kHeadDim + 4 * (l + 4 * i)) =
-          make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-    if (A.lse && l == 0) A.lse[at] = (m + log2f(sum)) * 0.69314718055994531f;
-    return;
-  }
-  uint16_t* dst = A.out + ((size_t)(sq.t0 + R / gq) * s.num_q_heads + kv * gq + R % gq) * kHeadDim;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<uint2*>(dst + 4 * (l + 4 * i)) =
-        make_uint2(pack_bf2(o[4 * i] * inv, o[4 * i + 1] * inv), pack_bf2(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
+__host__ __device__ constexpr int chunk_smem_bytes(bool shared_keys) {
+  return 1024 + (shared_keys ? 2 : 1) * kTileBytes16 + 2 * kStages * kTileBytes16 + (int)sizeof(ChunkCtrl);
 }
 
-template <int FMT>
-static cudaError_t launch_general(const ChunkAttnArgs& A, cudaStream_t st) {
+// --- mbarriers, tcgen05 ---------------------------------------------------
+
+__device__ __forceinline__ void bar_init(uint64_t* b, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+  return t;
+}
+// False when the wait was given up (here or by another thread of the CTA):
+// the caller leaves its loop, and the CTA ends with an error bit.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+  if (bar_try(b, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (!bar_try(b, parity)) {
+    if (*abort) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(b))
+               : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// 32 columns of the thread's lane -> 32 registers, starting at r.
+__device__ __forceinline__ void tc_ld32(float* r, uint32_t at) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tc_ld16(float* r, uint32_t at) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(at),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t at, const uint32_t* u) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(at), "r"(u[0]),
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle, 8-row groups 1024 bytes
+// apart; `lead` = bytes between blocks of 64 elements along the major axis.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// fp16 x fp16 -> fp32, M = N = 128; the value operand is stored with channels (N) contiguous.
+constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+
+// TMEM columns: S of the streams (P over it), then O of the streams.
+__device__ __forceinline__ uint32_t tm_s(uint32_t tmem, int i) { return tmem + 128 * i; }
+__device__ __forceinline__ uint32_t tm_o(uint32_t tmem, int i) { return tmem + 256 + 128 * i; }
+
+// --- the kernel -----------------------------------------------------------
+
+// What every thread of a CTA knows about its work.
+struct Work {
+  ChunkSeq sq;
+  int b, kv, gq, r0, rows, split;
+  int first, tiles;                          // tiles [first, first + tiles) of the range
+  int stream_tiles[2];
+};
+
+// Producer warp pw (0..3): subtiles 2 pw and 2 pw + 1 of every tile.
+template <int FMT, bool SHARED>
+__device__ __forceinline__ void produce(const ChunkAttnArgs& A, const Work& W, const TileRange& range, ChunkCtrl& C,
+                                        uint32_t k_tiles, uint32_t v_tiles, int pw) {
+  const kvq_cache& c = A.c;
+  const kvq_shape& s = c.shape;
+  const ChunkSeq& sq = W.sq;
+  const int lane = threadIdx.x & 31;
+  const bool rope = s.rope_theta > 0.f;
+  const bool direct = !rope && !s.sparse;    // whole quantized subtiles go straight from codes to halves
+  RawRows raw;
+  raw.slots = max(window_slots(s), 1);
+  raw.n = sq.n;
+  raw.total = sq.total;
+  raw.stride = (int64_t)s.num_kv_heads * kHeadDim;
+  const uint16_t* k_ring = (const uint16_t*)c.k_res + (is_token_cache(FMT) ? 0 : Addr::ring_row(s, W.b, W.kv, 0));
+  const uint16_t* v_ring = (const uint16_t*)c.v_res + (is_token_cache(FMT) ? 0 : Addr::ring_row(s, W.b, W.kv, 0));
+  const size_t at = ((size_t)sq.t0 * s.num_kv_heads + W.kv) * kHeadDim;
+  const uint16_t *k_new = A.k + at, *v_new = A.v + at;
+  const int p_last = sq.p0 + (min(W.r0 + (SHARED ? 2 : 1) * kRows, W.rows) - 1) / W.gq;
+
+  for (int g = 0; g < W.tiles; ++g) {
+    const int t0 = range.tile(W.first + g) * kKeys, st = g & 1;
+    const uint32_t parity = ((g >> 1) & 1) ^ 1;
+    TileInfo& info = C.info[g % kInfos];
+    // rows outside the window may see part of the tile only
+    const bool edge = A.window > 0 && t0 <= p_last - A.window && t0 + kKeys > A.sinks;
+    TileSrc d[2];
+    SubWords<FMT> w[2];
+    int mode[2];                             // 0 packed words in w, 1 bf16 rows, 2 anything, 3 none (bad page)
+    int quant[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int base = t0 + kTile * (2 * pw + i);
+      quant[i] = min(max(sq.nq - base, 0), kTile);
+      mode[i] = quant[i] == 0 ? 1 : (direct && quant[i] == kTile && !edge) ? 0 : 2;
+      if (quant[i] > 0 && !tile_src<FMT>(c, W.b, W.kv, base / kTile, d[i])) mode[i] = 3;
+      if (mode[i] == 0) load_sub<FMT>(d[i], w[i]);
+    }
+    if (!warp_wait(&C.k_empty[st], parity, &C.abort)) return;
+    const uint32_t kt = k_tiles + st * kTileBytes16, vt = v_tiles + st * kTileBytes16;
+    // The softmax reads the description when the scores are there: it has to
+    // be complete before the keys are handed over, so value rows that need a
+    // look (raw or mixed) are written first; their stage has to be free then.
+    bool v_free = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int sub = 2 * pw + i, base = t0 + kTile * sub;
+      int ek = 0, ev = 0, kind = 0;
+      uint32_t bad = 0u;
+      if (mode[i] == 0) {
+        if (FMT == 6 && d[i].bits == 2) keys_to_tile<FMT, 2>(w[i], kt, sub);
+        else keys_to_tile<FMT, SubWords<FMT>::kBits>(w[i], kt, sub);
+      } else {
+        if (!v_free) {
+          if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
+          v_free = true;
+        }
+        kind = FMT == 8 ? 1 : 0;
+        if (mode[i] == 3) {
+          if (lane == 0) atomicOr(c.err_word, KVQ_DEVERR_PAGE_RANGE);
+          zero_rows(kt, sub);
+          zero_rows(vt, sub);
+          bad = 1u << 16;
+        } else if (mode[i] == 1 && !rope) {
+          uint32_t none;
+          raw.ring = k_ring;
+          raw.fresh = k_new;
+          ek = rows_to_tile<true>(raw, base, kt, sub, none);
+          raw.ring = v_ring;
+          raw.fresh = v_new;
+          ev = rows_to_tile<false>(raw, base, vt, sub, bad);
+        } else {
+          raw.ring = k_ring;
+          raw.fresh = k_new;
+          ek = keys_any<FMT>(d[i], quant[i], raw, base, rope ? C.freq : nullptr, kt, sub);
+          raw.ring = v_ring;
+          raw.fresh = v_new;
+          ev = values_any<FMT>(d[i], quant[i], raw, base, vt, sub, bad);
+        }
+        if (ek != 0 || ev != 0 || bad != 0u) kind = 2;
+      }
+      if (lane == 0) {
+        const bool fp8 = FMT == 8 && mode[i] == 0;
+        const float vs = fp8 ? fmaxf(d[i].vs, 0x1p-100f) : scale_by(1.f, ev);
+        info.kmul[sub] = fp8 ? d[i].ks : scale_by(1.f, ek);
+        info.vlog[sub] = fp8 ? log2f(vs) : (float)ev;
+        info.vinv[sub] = fp8 ? 1.f / vs : scale_by(1.f, -ev);
+        info.bad[sub] = bad;
+        info.kind[sub] = (uint8_t)kind;
+      }
+    }
+    fence_async();
+    __syncwarp();
+    if (lane == 0) bar_arrive(&C.k_full[st]);
+    if (!v_free && !warp_wait(&C.v_empty[st], parity, &C.abort)) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (mode[i] != 0) continue;
+      if (FMT == 6 && d[i].bits == 2) values_to_tile<FMT, 2>(w[i], vt, 2 * pw + i);
+      else values_to_tile<FMT, SubWords<FMT>::kBits>(w[i], vt, 2 * pw + i);
+    }
+    fence_async();
+    __syncwarp();
+    if (lane == 0) bar_arrive(&C.v_full[st]);
+  }
+}
+
+// One thread issues every product.  Streams alternate, so that one stream's
+// softmax runs while the other's products do; a stream's next scores are
+// issued behind its P V, whose P they overwrite (the tensor core takes the
+// products of one thread in order).
+template <bool SHARED>
+__device__ __forceinline__ void issue(const Work& W, ChunkCtrl& C, uint32_t q_tiles, uint32_t k_tiles, uint32_t v_tiles) {
+  const uint32_t tmem = C.tmem;
+  const int streams = W.stream_tiles[1] > 0 ? 2 : 1;
+  volatile int* abort = &C.abort;
+  auto qk = [&](int i, int it) -> bool {
+    const int g = SHARED ? it : 2 * it + i, st = g & 1;
+    if (!SHARED || i == 0) {
+      if (!bar_wait(&C.k_full[st], (g >> 1) & 1, abort)) return false;
+      tc_after();
+    }
+    const uint32_t q = q_tiles + (SHARED ? i : 0) * kTileBytes16, k = k_tiles + st * kTileBytes16;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint32_t off = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
+      mma_ss(tm_s(tmem, i), operand_desc(q + off, 16), operand_desc(k + off, 16), kIdescQK, kk > 0);
+    }
+    if (!SHARED || i == streams - 1) tc_commit(&C.k_empty[st]);
+    tc_commit(&C.s_full[i]);
+    return true;
+  };
+  bool ok = true;
+  for (int i = 0; i < 2 && ok; ++i)
+    if (W.stream_tiles[i] > 0) ok = qk(i, 0);
+  for (int it = 0; it < W.stream_tiles[0] && ok; ++it) {
+    for (int i = 0; i < 2 && ok; ++i) {
+      if (it >= W.stream_tiles[i]) continue;
+      const int g = SHARED ? it : 2 * it + i, st = g & 1;
+      if (!(ok = bar_wait(&C.p_ready[i], it & 1, abort))) break;
+      if (!SHARED || i == 0) {
+        if (!(ok = bar_wait(&C.v_full[st], (g >> 1) & 1, abort))) break;
+      }
+      tc_after();
+      const uint32_t v = v_tiles + st * kTileBytes16;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(tm_o(tmem, i), tm_s(tmem, i) + 8 * kk, operand_desc(v + kk * 16 * 128, kBlockBytes), kIdescPV,
+               it > 0 || kk > 0);
+      if (!SHARED || i == streams - 1) tc_commit(&C.v_empty[st]);
+      if (it + 1 < W.stream_tiles[i]) ok = qk(i, it + 1);
+      else tc_commit(&C.o_done[i]);
+    }
+  }
+  if (!ok) {                                 // given up: let the products in flight end before TMEM is freed
+    tc_commit(&C.drained);
+    const unsigned long long t0 = now_ns();
+    while (!bar_try(&C.drained, 0) && now_ns() - t0 < kWaitNs) {}
+  }
+}
+
+struct RowState {
+  float m, l;                                // reference (log2 units) and sum of this thread's row
+};
+
+// The softmax of one tile for one stream; the thread owns one row.
+template <bool SHARED>
+__device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo& info, int t0, int p_row, int p_lo,
+                                          int p_hi, float cm, bool started, uint32_t ts, uint32_t to, RowState& r) {
+  const uint2 kinds = *reinterpret_cast<const uint2*>(info.kind);
+  // warp-uniform: every token of the tile is visible to every row, and the whole tile has one scaling
+  const bool plain = t0 + kKeys - 1 <= p_lo && (A.window <= 0 || t0 > p_hi - A.window || t0 + kKeys <= A.sinks) &&
+                     kinds.x == kinds.y && kinds.x == (kinds.x & 0xFFu) * 0x01010101u && (kinds.x & 0xFFu) != 2u;
+  auto raise = [&](float top) {              // the row's reference, and O with it if it moves
+    const bool up = top > r.m + kSlack || (r.m == -INFINITY && top > -INFINITY);
+    const float mn = up ? top : r.m;
+    const float f = r.m == -INFINITY ? (up ? 0.f : 1.f) : (up ? ex2(r.m - mn) : 1.f);
+    if (started && __any_sync(0xffffffffu, up && r.m != -INFINITY)) {
+      // the scores are complete, so the products before them are: O is at rest
+      const float fo = r.m == -INFINITY ? 1.f : f;             // O is zero then
+#pragma unroll 1
+      for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
+        float o[16];
+        tc_ld16(o, to + c0);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] *= fo;
+        tc_st16(to + c0, reinterpret_cast<uint32_t*>(o));
+      }
+      tc_wait_st();
+    }
+    r.l *= f;
+    r.m = mn;
+  };
+  if (plain) {
+    // two passes over the scores in TMEM, 64 columns in registers at a time
+    const float k = cm * info.kmul[0], vlog = info.vlog[0];
+    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c0 = 0; c0 < kKeys; c0 += 64) {
+      float x[64];
+      tc_ld32(x, ts + c0);
+      tc_ld32(x + 32, ts + c0 + 32);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 64; i += 8) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) t4[u] = fmaxf(t4[u], fmaxf(x[i + 2 * u], x[i + 2 * u + 1]));
+      }
+    }
+    raise(fmaf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), k, vlog));
+    const float off = vlog - (r.m == -INFINITY ? 0.f : r.m);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c0 = 0; c0 < kKeys; c0 += 64) {
+      float x[64];
+      tc_ld32(x, ts + c0);
+      tc_ld32(x + 32, ts + c0 + 32);
+      tc_wait_ld();
+#pragma unroll
+      for (int c1 = 0; c1 < 64; c1 += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float a = ex2(fmaf(x[c1 + 2 * i], k, off)), b = ex2(fmaf(x[c1 + 2 * i + 1], k, off));
+          sum[(2 * i) & 3] += a;
+          sum[(2 * i + 1) & 3] += b;
+          p[i] = pack_h2(a, b);
+        }
+        tc_st16(ts + (c0 + c1) / 2, p);
+      }
+    }
+    r.l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), info.vinv[0], r.l);
+  } else {
+    // subtile by subtile: its own scaling, hidden and missing tokens left out
+    auto scores = [&](int sub, float (&x)[16]) {
+      tc_ld16(x, ts + kTile * sub);
+      tc_wait_ld();
+      const float k = cm * info.kmul[sub], vlog = info.vlog[sub];
+      const bool none = info.bad[sub] >> 16;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const int t = t0 + kTile * sub + row_of_token(c);      // the order is its own inverse
+        x[c] = !none && key_visible(t, p_row, A.window, A.sinks) ? fmaf(x[c], k, vlog) : -INFINITY;
+      }
+    };
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int sub = 0; sub < kSubs; ++sub) {
+      float x[16];
+      scores(sub, x);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) top = fmaxf(top, x[c]);
+    }
+    raise(top);
+    const float ref = r.m == -INFINITY ? 0.f : r.m;
+    float l = 0.f;
+#pragma unroll 1
+    for (int sub = 0; sub < kSubs; ++sub) {
+      float x[16], sum = 0.f;
+      scores(sub, x);
+      const uint32_t bad = info.bad[sub];
+      uint32_t p[8];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        if ((bad >> c & 1u) && x[c] != -INFINITY) sum = __int_as_float(0x7FC00000);   // the row sees such a value
+        x[c] = ex2(x[c] - ref);
+        sum += x[c];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = pack_h2(x[2 * i], x[2 * i + 1]);
+      tc_st8(ts + 8 * sub, p);
+      l = fmaf(sum, info.vinv[sub], l);
+    }
+    r.l += l;
+  }
+}
+
+// Row r (m, l, O) of stream i -> the caller's output, or this split's partial.
+__device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W, int R, const RowState& r, uint32_t to,
+                                          bool any, const float* other, const float* f) {
   const kvq_shape& s = A.c.shape;
-  const int gq = s.num_q_heads / s.num_kv_heads;
-  cudaError_t e = cudaFuncSetAttribute(chunk_general_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(GenSmem));
+  const bool mine = R < W.rows;
+  const size_t row = mine ? (size_t)(W.sq.t0 + R / W.gq) * s.num_q_heads + W.kv * W.gq + R % W.gq : 0;
+  const bool partial = A.splits > 1;
+  const float inv = partial ? 1.f : (r.l > 0.f ? 1.f / r.l : (r.l == 0.f ? 0.f : r.l));
+  const size_t slot = (size_t)W.split * A.rows * s.num_q_heads + row;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+    float o[32];
+    if (any) {                               // warp-uniform
+      tc_ld32(o, to + c0);
+      tc_wait_ld();
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = any && r.l != 0.f ? o[i] * f[0] * inv : 0.f;
+    if (other) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(other + 4 * (((c0 / 4) + i) ^ (threadIdx.x & 31)));
+        o[4 * i] = fmaf(x.x, f[1] * inv, o[4 * i]); o[4 * i + 1] = fmaf(x.y, f[1] * inv, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(x.z, f[1] * inv, o[4 * i + 2]); o[4 * i + 3] = fmaf(x.w, f[1] * inv, o[4 * i + 3]);
+      }
+    }
+    if (!mine) continue;
+    if (partial || A.out32) {
+      float4* dst = reinterpret_cast<float4*>(partial ? A.ws_o + slot * kHeadDim + c0 : A.out32 + row * kHeadDim + c0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(A.out + row * kHeadDim + c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dst[i] = make_uint4(pack_bf2(o[8 * i], o[8 * i + 1]), pack_bf2(o[8 * i + 2], o[8 * i + 3]),
+                            pack_bf2(o[8 * i + 4], o[8 * i + 5]), pack_bf2(o[8 * i + 6], o[8 * i + 7]));
+    }
+  }
+  if (!mine) return;
+  if (partial) *reinterpret_cast<float2*>(A.ws_ml + 2 * slot) = make_float2(r.m, r.l);
+  else if (A.lse) A.lse[row] = (r.m + log2f(r.l)) * 0.69314718055994531f;
+}
+
+// Grid (row blocks x splits, H_kv, B), 13 warps, one CTA per SM.
+// SHARED: 256 query rows, a stream for each half, every key tile serves both.
+// Otherwise 128 rows at most: both streams have the same rows, stream i takes
+// the tiles of parity i, and the halves of the sum are joined at the end.
+template <int FMT, bool SHARED>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(ChunkAttnArgs A) {
+  extern __shared__ uint8_t smem_raw[];
+  grid_dependents_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const kvq_shape& s = A.c.shape;
+  constexpr int kBlockRows = (SHARED ? 2 : 1) * kRows;
+  Work W;
+  W.kv = blockIdx.y;
+  W.b = blockIdx.z;
+  W.gq = s.num_q_heads / s.num_kv_heads;
+  W.split = blockIdx.x % A.splits;
+  W.r0 = (int)(gridDim.x / A.splits - 1 - blockIdx.x / A.splits) * kBlockRows;   // the longest rows first
+  W.sq = chunk_seq(A, W.b);
+  W.rows = W.sq.m * W.gq;
+  if (W.sq.err && blockIdx.x == 0 && W.kv == 0 && tid == 0) atomicOr(A.c.err_word, W.sq.err);
+  if (W.r0 >= W.rows) return;
+  const int block_rows = min(kBlockRows, W.rows - W.r0);
+  const TileRange range(W.sq.p0 + W.r0 / W.gq, W.sq.p0 + (W.r0 + block_rows - 1) / W.gq, A.window, A.sinks, kKeys);
+  W.first = (int)((int64_t)range.count * W.split / A.splits);
+  W.tiles = (int)((int64_t)range.count * (W.split + 1) / A.splits) - W.first;
+  if (SHARED) {
+    W.stream_tiles[0] = W.tiles;
+    W.stream_tiles[1] = block_rows > kRows ? W.tiles : 0;
+  } else {
+    W.stream_tiles[0] = (W.tiles + 1) / 2;
+    W.stream_tiles[1] = W.tiles / 2;
+  }
+
+  const uint32_t q_tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t k_tiles = q_tiles + (SHARED ? 2 : 1) * kTileBytes16, v_tiles = k_tiles + kStages * kTileBytes16;
+  uint8_t* generic = smem_raw + (q_tiles - smem_u32(smem_raw));
+  ChunkCtrl& C = *reinterpret_cast<ChunkCtrl*>(generic + (v_tiles + kStages * kTileBytes16 - q_tiles));
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(&C.k_full[i], 4); bar_init(&C.k_empty[i], 1);
+      bar_init(&C.v_full[i], 4); bar_init(&C.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) { bar_init(&C.s_full[i], 1); bar_init(&C.p_ready[i], 4); bar_init(&C.o_done[i], 1); }
+    bar_init(&C.drained, 1);
+    C.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&C.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  if (s.rope_theta > 0.f && warp == kMmaWarp) {
+    for (int i = lane; i < kHeadDim / 2; i += 32) C.freq[i] = pow((double)s.rope_theta, -2.0 * i / kHeadDim);
+  }
+  // Query rows -> fp16 in the key tiles' channel order, powers of two aside
+  // (they go into the row's factor), negated for a negative scale.
+  if (warp < 4 || (SHARED && warp < 8)) {
+    const int R = min(W.r0 + tid, W.rows - 1);               // rows past the end repeat the last one
+    const uint4* src = reinterpret_cast<const uint4*>(
+        A.q + ((size_t)(W.sq.t0 + R / W.gq) * s.num_q_heads + W.kv * W.gq + R % W.gq) * kHeadDim);
+    float amax = 0.f;
+    uint4 w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = src[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x[8];
+      unpack8(w[i], x);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) amax = fmaxf(amax, finite_abs(x[u]));
+    }
+    const int e = tile_exponent(amax);
+    const float sign = A.scale_log2 < 0.f ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x[8];
+      unpack8(w[i], x);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = sign * (e ? scale_by(x[u], -e) : x[u]);
+      put_key8(q_tiles + (tid / kRows) * kTileBytes16, tid % kRows, i, x);
+    }
+    C.qmul[tid] = scale_by(1.f, e);
+    fence_async();
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = C.tmem;
+
+  if (warp >= kProducerWarp && warp < kMmaWarp) {
+    produce<FMT, SHARED>(A, W, range, C, k_tiles, v_tiles, warp - kProducerWarp);
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) issue<SHARED>(W, C, q_tiles, k_tiles, v_tiles);
+    __syncwarp();
+  } else {
+    const int i = warp >> 2, row = tid % kRows, R = W.r0 + (SHARED ? i * kRows : 0) + row;
+    const int last = W.rows - 1;
+    const int w0 = W.r0 + (SHARED ? i * kRows : 0) + 32 * (warp & 3);      // the warp's first row
+    const bool idle = w0 > last;
+    const int p_row = W.sq.p0 + min(R, last) / W.gq;
+    const int p_lo = W.sq.p0 + min(w0, last) / W.gq, p_hi = W.sq.p0 + min(w0 + 31, last) / W.gq;
+    const float cm = fabsf(A.scale_log2) * C.qmul[SHARED ? tid : row];
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tm_s(tmem, i) + lanes, to = tm_o(tmem, i) + lanes;
+    RowState r{-INFINITY, 0.f};
+    bool ok = true;
+    for (int it = 0; it < W.stream_tiles[i]; ++it) {
+      const int g = SHARED ? it : 2 * it + i;
+      if (!(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
+      if (!idle) {
+        tc_after();
+        soft_tile<SHARED>(A, C.info[g % kInfos], range.tile(W.first + g) * kKeys, p_row, p_lo, p_hi, cm, it > 0, ts, to,
+                          r);
+        tc_wait_st();
+        tc_before();
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(&C.p_ready[i]);
+    }
+    const bool any = W.stream_tiles[i] > 0;
+    if (ok && any) ok = warp_wait(&C.o_done[i], 0, &C.abort);
+    tc_after();
+    const float one[2] = {1.f, 0.f};
+    if (SHARED) {
+      if (ok && !idle) store_row(A, W, R, r, to, any, nullptr, one);
+    } else {
+      // join the streams: stream 1's row through shared memory (the tiles are used up)
+      float* o1 = reinterpret_cast<float*>(generic + kTileBytes16) + row * kHeadDim;
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      if (i == 1) {
+        C.ml[row][0] = r.m;
+        C.ml[row][1] = r.l;
+        if (ok && any && !idle) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+            float o[32];
+            tc_ld32(o, to + c0);
+            tc_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<float4*>(o1 + 4 * ((c0 / 4 + u) ^ lane)) =
+                  make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          }
+        }
+      }
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      if (i == 0 && ok && !idle) {
+        const float m1 = C.ml[row][0], l1 = C.ml[row][1];
+        const bool two = W.stream_tiles[1] > 0;
+        const float M = fmaxf(r.m, m1), ref = M == -INFINITY ? 0.f : M;
+        const float f[2] = {ex2(r.m - ref), two && m1 != -INFINITY ? ex2(m1 - ref) : 0.f};
+        RowState j{M, r.l * f[0] + (two ? l1 * f[1] : 0.f)};
+        store_row(A, W, R, j, to, any, two ? o1 : nullptr, f);
+      }
+    }
+    tc_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+  if (tid == 0 && C.abort) atomicOr(A.c.err_word, KVQ_DEVERR_WAIT_TIMEOUT);
+}
+
+// Joins the splits' partials.  Grid (rows of a sequence / 8, B), one warp per
+// (new token, query head) row, four channels per lane.
+__global__ void __launch_bounds__(256) chunk_merge_kernel(ChunkAttnArgs A) {
+  grid_dependency_wait();
+  const kvq_shape& s = A.c.shape;
+  const ChunkSeq sq = chunk_seq(A, blockIdx.y);
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= (int64_t)sq.m * s.num_q_heads) return;
+  const size_t row = (size_t)sq.t0 * s.num_q_heads + i, rows = (size_t)A.rows * s.num_q_heads;
+  float M = -INFINITY;
+  for (int p = 0; p < A.splits; ++p) M = fmaxf(M, A.ws_ml[2 * (p * rows + row)]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < A.splits; ++p) {
+    const float2 ml = *reinterpret_cast<const float2*>(A.ws_ml + 2 * (p * rows + row));
+    if (ml.y == 0.f) continue;               // nothing visible in this range (NaN goes on)
+    const float f = ex2(ml.x - ref);
+    const float4 x = *reinterpret_cast<const float4*>(A.ws_o + (p * rows + row) * kHeadDim + 4 * lane);
+    l = fmaf(ml.y, f, l);
+    o.x = fmaf(x.x, f, o.x); o.y = fmaf(x.y, f, o.y); o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+  if (A.out32) {
+    *reinterpret_cast<float4*>(A.out32 + row * kHeadDim + 4 * lane) = o;
+    if (A.lse && lane == 0) A.lse[row] = (M + log2f(l)) * 0.69314718055994531f;
+  } else {
+    *reinterpret_cast<uint2*>(A.out + row * kHeadDim + 4 * lane) = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
+  }
+}
+
+// --- host -----------------------------------------------------------------
+
+static bool shared_keys(const kvq_shape& s, int max_new) {
+  return (long long)max_new * (s.num_q_heads / s.num_kv_heads) > kRows;
+}
+static long long row_blocks(const kvq_shape& s, int max_new) {
+  const long long rows = (long long)max_new * (s.num_q_heads / s.num_kv_heads);
+  const int block = shared_keys(s, max_new) ? 2 * kRows : kRows;
+  return (rows + block - 1) / block;
+}
+
+size_t chunk_workspace_bytes(const kvq_shape& s, int num_splits, int rows) {
+  if (num_splits <= 1) return 0;
+  return (size_t)num_splits * rows * s.num_q_heads * (kHeadDim + 2) * sizeof(float);
+}
+
+// Key ranges per row block: the fewest rounds of CTAs over the SMs, counting
+// what a CTA costs beside its tiles (set-up and output, worth about four
+// tiles).
+int chunk_default_splits(const kvq_shape& s, int rows, int max_new, int max_len, int window, int sinks) {
+  const long long span = window > 0 ? min((long long)max_len + max_new, (long long)window + sinks + max_new)
+                                    : (long long)max_len + max_new;
+  const int tiles = (int)((span + kKeys - 1) / kKeys) + 1;
+  const long long ctas = row_blocks(s, max_new) * s.num_kv_heads * min(s.batch, max(rows, 1));
+  int best = 1;
+  double least = 1e30;
+  for (int n = 1; n <= 64 && n <= tiles; ++n) {
+    const long long rounds = (ctas * n + 147) / 148;
+    const double t = (double)rounds * ((tiles + n - 1) / n + 4 + (n > 1 ? 1 : 0));
+    if (t < least * 0.97) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
+}
+
+template <int FMT, bool SHARED>
+static cudaError_t launch_form(const ChunkAttnArgs& A, cudaStream_t st) {
+  const kvq_shape& s = A.c.shape;
+  constexpr int kSmem = chunk_smem_bytes(SHARED);
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+  cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<FMT, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmem);
   if (e != cudaSuccess) return e;
-  const long long blocks = ((long long)min(A.max_new, A.rows) * gq + kGenRows - 1) / kGenRows;
-  dim3 grid((unsigned)max(blocks, 1ll), s.num_kv_heads, s.batch);
-  chunk_general_kernel<FMT><<<grid, 128, sizeof(GenSmem), st>>>(A);
+  const long long x = row_blocks(s, min(A.max_new, A.rows)) * A.splits;
+  if (x > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  dim3 grid((unsigned)max(x, 1ll), s.num_kv_heads, s.batch);
+  chunk_attention_kernel<FMT, SHARED><<<grid, kChunkThreads, kSmem, st>>>(A);
   return cudaGetLastError();
 }
 
-size_t chunk_workspace_bytes(const kvq_shape& s, int num_splits, int rows) { return 0; }
-int chunk_default_splits(const kvq_shape& s, int rows, int max_new, int max_len, int window, int sinks) { return 1; }
-
-cudaError_t launch_chunk_attention(const ChunkAttnArgs& A, cudaStream_t st) {
-  switch (A.c.shape.format) {
-    case KVQ_FORMAT_INT2: return launch_general<2>(A, st);
-    case KVQ_FORMAT_INT4: return launch_general<4>(A, st);
-    case KVQ_FORMAT_MIXED: return launch_general<6>(A, st);
-    case KVQ_FORMAT_FP8_E4M3: return launch_general<8>(A, st);
-    default: return launch_general<16>(A, st);
+cudaError_t launch_chunk_attention(const ChunkAttnArgs& args, cudaStream_t st) {
+  ChunkAttnArgs A = args;
+  const kvq_shape& s = A.c.shape;
+  const size_t rows = (size_t)A.rows * s.num_q_heads;
+  A.ws_ml = A.ws_o ? A.ws_o + (size_t)A.splits * rows * kHeadDim : nullptr;
+  const bool wide = shared_keys(s, min(A.max_new, A.rows));
+  cudaError_t e;
+#define KVQ_CHUNK_FORM(F) (wide ? launch_form<F, true>(A, st) : launch_form<F, false>(A, st))
+  switch (s.format) {
+    case KVQ_FORMAT_INT2: e = KVQ_CHUNK_FORM(2); break;
+    case KVQ_FORMAT_INT4: e = KVQ_CHUNK_FORM(4); break;
+    case KVQ_FORMAT_MIXED: e = KVQ_CHUNK_FORM(6); break;
+    case KVQ_FORMAT_FP8_E4M3: e = KVQ_CHUNK_FORM(8); break;
+    default: e = KVQ_CHUNK_FORM(16); break;
   }
+#undef KVQ_CHUNK_FORM
+  if (e != cudaSuccess || A.splits == 1) return e;
+  const long long per_seq = (long long)min(A.max_new, A.rows) * s.num_q_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((per_seq + 7) / 8), s.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  pdl_attribute(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, A);
 }
 
 }  // namespace kvq
