@@ -406,7 +406,8 @@ def _prepare_own(case, x, st):
     st["cu"], st["cu_new"] = _offsets(held), _offsets(new)
     st["total"] = _offsets([n + m for n, m in zip(held, new)])
     if case["fmt"] == 8:
-        c.region("fp8_scale").view(torch.float32).copy_(x["scale"].flatten())
+        scale = c.region("fp8_scale").view(torch.float32)[: 2 * case["hkv"]]   # the buffer is padded to 16 bytes
+        scale.copy_(x["scale"].flatten())
     if case["op"] == "write":
         rows = sum(held) + sum(new)
         st["out"] = [torch.empty(rows, case["hkv"], D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
