@@ -26,6 +26,9 @@ cudaError_t launch_chunk_attention(const ChunkAttnArgs& A, cudaStream_t st);
 int chunk_default_splits(const kvq_shape& s, int rows, int max_new, int max_len, int window, int sinks);
 size_t chunk_workspace_bytes(const kvq_shape& s, int num_splits, int rows);
 int decode_default_splits(const kvq_shape& s, int max_len);
+int window_default_splits(const kvq_shape& s, int max_len, int window, int sinks);
+cudaError_t launch_window_decode(const kvq_cache& c, const void* q, float* out, float* lse, float softmax_scale,
+                                 int window, int sinks, void* ws, int num_splits, cudaStream_t st);
 size_t decode_workspace_bytes(const kvq_shape& s, int num_splits);
 }  // namespace kvq
 
@@ -306,52 +309,11 @@ kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q_bf16, const
   A.v = (const uint16_t*)v_new_bf16;
   A.cu = cu_seqlens_dev;
   A.out = (uint16_t*)out_bf16;
-  A.out32 = A.lse = nullptr;
   A.ws_o = (float*)workspace;
   A.ws_ml = nullptr;
   A.scale_log2 = softmax_scale * 1.4426950408889634f;
   A.rows = total_new;
   A.max_new = max_new;
-  A.window = window;
-  A.sinks = sinks;
-  A.splits = splits;
-  return from_cuda(launch_chunk_attention(A, (cudaStream_t)stream));
-}
-
-// Split count of a windowed decode call (0 = the library's choice), or 0 if an argument is out of range.
-static int window_splits(const kvq_shape& s, int32_t num_splits, int32_t max_len, int32_t window, int32_t sinks) {
-  return chunk_splits(s, num_splits, s.batch, 1, max_len, window, sinks);
-}
-
-size_t kvq_window_workspace_bytes(const kvq_cache* cache, int32_t num_splits, int32_t max_len, int32_t window,
-                                  int32_t sinks) {
-  if (!cache || check_shape(&cache->shape) != KVQ_OK) return 0;
-  const int splits = window_splits(cache->shape, num_splits, max_len, window, sinks);
-  return splits ? chunk_workspace_bytes(cache->shape, splits, cache->shape.batch) : 0;
-}
-
-kvq_status kvq_decode_attention_window(const kvq_cache* cache, const void* q_bf16, float* out, float* lse,
-                                       float softmax_scale, int32_t window, int32_t sinks, void* workspace,
-                                       size_t ws_bytes, int32_t num_splits, int32_t max_len, kvq_stream_t stream) {
-  kvq_status st = check_cache(cache);
-  if (st != KVQ_OK) return st;
-  if (!q_bf16 || !out || !(softmax_scale == softmax_scale)) return KVQ_ERR_INVALID_ARG;
-  const kvq_shape& s = cache->shape;
-  const int splits = window_splits(s, num_splits, max_len, window, sinks);
-  if (!splits) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(q_bf16) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
-  const size_t need = chunk_workspace_bytes(s, splits, s.batch);
-  if (need > 0 && !workspace) return KVQ_ERR_INVALID_ARG;
-  if (ws_bytes < need) return KVQ_ERR_WORKSPACE;
-  ChunkAttnArgs A = {};
-  A.c = *cache;
-  A.q = (const uint16_t*)q_bf16;
-  A.out32 = out;
-  A.lse = lse;
-  A.ws_o = (float*)workspace;
-  A.scale_log2 = softmax_scale * 1.4426950408889634f;
-  A.rows = s.batch;
-  A.max_new = 1;
   A.window = window;
   A.sinks = sinks;
   A.splits = splits;
@@ -418,6 +380,33 @@ kvq_status kvq_decode_attention_lse(const kvq_cache* cache, const void* q_bf16, 
                                     int32_t max_len, kvq_stream_t stream) {
   if (!lse) return KVQ_ERR_INVALID_ARG;
   return decode_checked(cache, q_bf16, out, lse, softmax_scale, workspace, ws_bytes, num_splits, max_len, stream);
+}
+
+// Split count of a windowed decode (0 = the library's choice), or 0 if an argument is out of range.
+static int window_splits(const kvq_shape& s, int32_t num_splits, int32_t max_len, int32_t window, int32_t sinks) {
+  if (num_splits < 0 || num_splits > 65535 || max_len < 0 || window < 0 || sinks < 0) return 0;
+  return num_splits > 0 ? num_splits : window_default_splits(s, max_len, window, sinks);
+}
+
+size_t kvq_window_workspace_bytes(const kvq_cache* cache, int32_t num_splits, int32_t max_len, int32_t window,
+                                  int32_t sinks) {
+  if (!cache || check_shape(&cache->shape) != KVQ_OK) return 0;
+  const int splits = window_splits(cache->shape, num_splits, max_len, window, sinks);
+  return splits ? decode_workspace_bytes(cache->shape, splits) : 0;
+}
+
+kvq_status kvq_decode_attention_window(const kvq_cache* cache, const void* q_bf16, float* out, float* lse,
+                                       float softmax_scale, int32_t window, int32_t sinks, void* workspace,
+                                       size_t ws_bytes, int32_t num_splits, int32_t max_len, kvq_stream_t stream) {
+  int32_t splits = 1;
+  kvq_status st = decode_validate(cache, q_bf16, out, lse, softmax_scale, num_splits, max_len, &splits);
+  if (st != KVQ_OK) return st;
+  splits = window_splits(cache->shape, num_splits, max_len, window, sinks);
+  if (!splits || !workspace) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  if (ws_bytes < decode_workspace_bytes(cache->shape, splits)) return KVQ_ERR_WORKSPACE;
+  return from_cuda(launch_window_decode(*cache, q_bf16, out, lse, softmax_scale, window, sinks, workspace, splits,
+                                        (cudaStream_t)stream));
 }
 
 kvq_status kvq_merge_partials(const float* outs, const float* lses, int32_t parts, int64_t rows, float* out,

@@ -1,6 +1,5 @@
-// kvq_chunk_attention and kvq_decode_attention_window: query rows against the
-// packed cache (and causally against the chunk's own tokens) on the tensor
-// cores.
+// kvq_chunk_attention: a chunk's query rows against the packed cache and,
+// causally, against the chunk's own tokens, on the tensor cores.
 //
 // Per (sequence, kv head) the query rows of all gq heads and new tokens form
 // one matrix (row R = head R % gq of token R / gq).  For each tile of 128
@@ -176,7 +175,7 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, const Work& W, c
   const uint16_t* v_ring = (const uint16_t*)c.v_res + (is_token_cache(FMT) ? 0 : Addr::ring_row(s, W.b, W.kv, 0));
   const size_t at = ((size_t)sq.t0 * s.num_kv_heads + W.kv) * kHeadDim;
   const uint16_t *k_new = A.k + at, *v_new = A.v + at;
-  const int p_last = sq.p0 + (min(W.r0 + (SHARED ? 2 : 1) * kRows, W.rows) - 1) / W.gq;
+  const int p_last = sq.n + (min(W.r0 + (SHARED ? 2 : 1) * kRows, W.rows) - 1) / W.gq;
 
   for (int g = 0; g < W.tiles; ++g) {
     const int t0 = range.tile(W.first + g) * kKeys, st = g & 1;
@@ -463,8 +462,8 @@ __device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W,
       }
     }
     if (!mine) continue;
-    if (partial || A.out32) {
-      float4* dst = reinterpret_cast<float4*>(partial ? A.ws_o + slot * kHeadDim + c0 : A.out32 + row * kHeadDim + c0);
+    if (partial) {
+      float4* dst = reinterpret_cast<float4*>(A.ws_o + slot * kHeadDim + c0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     } else {
@@ -475,9 +474,7 @@ __device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W,
                             pack_bf2(o[8 * i + 4], o[8 * i + 5]), pack_bf2(o[8 * i + 6], o[8 * i + 7]));
     }
   }
-  if (!mine) return;
-  if (partial) *reinterpret_cast<float2*>(A.ws_ml + 2 * slot) = make_float2(r.m, r.l);
-  else if (A.lse) A.lse[row] = (r.m + log2f(r.l)) * 0.69314718055994531f;
+  if (mine && partial) *reinterpret_cast<float2*>(A.ws_ml + 2 * slot) = make_float2(r.m, r.l);
 }
 
 // Grid (row blocks x splits, H_kv, B), 13 warps, one CTA per SM.
@@ -502,7 +499,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(Chunk
   if (W.sq.err && blockIdx.x == 0 && W.kv == 0 && tid == 0) atomicOr(A.c.err_word, W.sq.err);
   if (W.r0 >= W.rows) return;
   const int block_rows = min(kBlockRows, W.rows - W.r0);
-  const TileRange range(W.sq.p0 + W.r0 / W.gq, W.sq.p0 + (W.r0 + block_rows - 1) / W.gq, A.window, A.sinks, kKeys);
+  const TileRange range(W.sq.n + W.r0 / W.gq, W.sq.n + (W.r0 + block_rows - 1) / W.gq, A.window, A.sinks, kKeys);
   W.first = (int)((int64_t)range.count * W.split / A.splits);
   W.tiles = (int)((int64_t)range.count * (W.split + 1) / A.splits) - W.first;
   if (SHARED) {
@@ -579,8 +576,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(Chunk
     const int last = W.rows - 1;
     const int w0 = W.r0 + (SHARED ? i * kRows : 0) + 32 * (warp & 3);      // the warp's first row
     const bool idle = w0 > last;
-    const int p_row = W.sq.p0 + min(R, last) / W.gq;
-    const int p_lo = W.sq.p0 + min(w0, last) / W.gq, p_hi = W.sq.p0 + min(w0 + 31, last) / W.gq;
+    const int p_row = W.sq.n + min(R, last) / W.gq;
+    const int p_lo = W.sq.n + min(w0, last) / W.gq, p_hi = W.sq.n + min(w0 + 31, last) / W.gq;
     const float cm = fabsf(A.scale_log2) * C.qmul[SHARED ? tid : row];
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm_s(tmem, i) + lanes, to = tm_o(tmem, i) + lanes;
@@ -670,12 +667,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(ChunkAttnArgs A) {
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-  if (A.out32) {
-    *reinterpret_cast<float4*>(A.out32 + row * kHeadDim + 4 * lane) = o;
-    if (A.lse && lane == 0) A.lse[row] = (M + log2f(l)) * 0.69314718055994531f;
-  } else {
-    *reinterpret_cast<uint2*>(A.out + row * kHeadDim + 4 * lane) = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
-  }
+  *reinterpret_cast<uint2*>(A.out + row * kHeadDim + 4 * lane) = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
 }
 
 // --- host -----------------------------------------------------------------

@@ -12,9 +12,6 @@ struct ChunkAttnArgs {
   const uint16_t* v;      // bf16 [rows][H_kv][128]
   const int32_t* cu;      // [B + 1] chunk rows of each sequence
   uint16_t* out;          // bf16 [rows][H_q][128]
-  // decode form (out32 set): one row per sequence at position seq_len - 1, no chunk
-  float* out32;           // [B][H_q][128]
-  float* lse;             // [B][H_q], or null
   float* ws_o;            // [splits][rows][H_q][128] (splits > 1)
   float* ws_ml;           // [splits][rows][H_q][2]
   float scale_log2;       // softmax_scale * log2(e)
@@ -24,28 +21,26 @@ struct ChunkAttnArgs {
   int splits;
 };
 
-// The sequence's share of a call: cached tokens n (nq quantized), m query rows
-// from row t0 on at positions p0, p0 + 1, ..., `total` tokens with the chunk's.
-// err: the bit to report for a state, length or row range that fails the
-// checks (then m = 0 and nothing is computed).
+// The sequence's share of a call: n cached tokens (nq quantized), m new ones
+// from row t0 on at positions n, n + 1, ..., `total` together.  err: the bit
+// to report for a state, length or row range that fails the checks (then m =
+// 0 and nothing is computed).
 struct ChunkSeq {
-  int n, nq, m, t0, p0, total;
+  int n, nq, m, t0, total;
   uint32_t err;
 };
 
 __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkAttnArgs& A, int b) {
   ChunkSeq q;
-  const bool decode = A.out32 != nullptr;
-  q.t0 = decode ? b : A.cu[b];
-  q.m = decode ? 1 : A.cu[b + 1] - q.t0;
+  q.t0 = A.cu[b];
+  q.m = A.cu[b + 1] - q.t0;
   q.n = A.c.seq_len[b];
   q.nq = A.c.n_quant[b];
   q.err = 0u;
   if (state_bad(A.c.shape, q.n, q.nq)) q.err = KVQ_DEVERR_STATE;
   else if (q.m < 0 || q.m > A.max_new || q.t0 < 0 || q.t0 > A.rows - q.m) q.err = KVQ_DEVERR_PREFILL_LEN;
   if (q.err) q.m = 0;
-  q.p0 = decode ? q.n - 1 : q.n;
-  q.total = decode ? q.n : q.n + q.m;
+  q.total = q.n + q.m;
   return q;
 }
 
@@ -58,7 +53,7 @@ struct TileRange {
     const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
     skip = lo / TS;
     lead = min(skip, (min(sinks, lo) + TS - 1) / TS);
-    count = p1 < 0 ? 0 : lead + p1 / TS + 1 - skip;
+    count = lead + p1 / TS + 1 - skip;
   }
   __device__ __forceinline__ int tile(int i) const { return i < lead ? i : skip + i - lead; }
 };

@@ -103,7 +103,7 @@ typedef enum {
 #define KVQ_DEVERR_APPEND_FULL   0x1u   /* append found the capacity or the window full; token dropped */
 #define KVQ_DEVERR_PAGE_RANGE    0x2u   /* a page id outside [0, num_pages); that page skipped */
 #define KVQ_DEVERR_PREFILL_LEN   0x4u   /* a prefill sequence longer than the capacity; skipped */
-#define KVQ_DEVERR_WAIT_TIMEOUT  0x8u   /* reserved: no current kernel waits on another (copies complete in hardware) */
+#define KVQ_DEVERR_WAIT_TIMEOUT  0x8u   /* a kernel gave up a wait between its own warps (2 s); the rows concerned are undefined */
 #define KVQ_DEVERR_STATE         0x10u  /* seq_len / n_quant inconsistent; unit skipped */
 
 /* Cache shape.  head_dim must be 128.  INT2/INT4: group % 16 == 0,
@@ -487,13 +487,12 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache *cache, int32_t num_splits, int
  *  lse:        float [B][H_q], or NULL
  *  window, sinks: >= 0
  *  workspace:  kvq_window_workspace_bytes(cache, num_splits, max_len, window,
- *              sinks) bytes, as kvq_chunk_attention's; may be NULL if that is 0.
- *  num_splits: >= 1: the visible keys are cut into that many ranges; 0 = the
- *              library's choice.
- *  max_len:    an upper bound of seq_len over the batch (for that choice).
- * A sequence without tokens gets out = 0 and lse = -inf; one with an
- * inconsistent state (KVQ_DEVERR_STATE) is skipped, its rows left as they
- * were; a page whose id is out of range is left out (KVQ_DEVERR_PAGE_RANGE).
+ *              sinks) bytes
+ *  num_splits, max_len: as for kvq_decode_attention (0 splits: chosen for the
+ *              tokens that can be visible).
+ * A sequence without tokens, or with an inconsistent state
+ * (KVQ_DEVERR_STATE), gets out = 0 and lse = -inf; a page whose id is out of
+ * range is left out (KVQ_DEVERR_PAGE_RANGE).
  */
 kvq_status kvq_decode_attention_window(const kvq_cache *cache, const void *q_bf16, float *out, float *lse,
                                        float softmax_scale, int32_t window, int32_t sinks, void *workspace,
