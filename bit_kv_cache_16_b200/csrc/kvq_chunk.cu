@@ -14,9 +14,8 @@
 namespace kvq {
 
 constexpr int kRows = 128;                   // query rows per stream: one TMEM lane and one softmax thread each
-constexpr int kProducerWarp = 8;             // warps 0-3 and 4-7: softmax of streams 0 and 1; 8-11: producers
-constexpr int kMmaWarp = 12;
-constexpr int kChunkThreads = 32 * (kMmaWarp + 1);
+constexpr int kProducerWarp = 8;             // warps 0-3 and 4-7: softmax of streams 0 and 1; 8-15: producers
+constexpr int kChunkThreads = 32 * (kProducerWarp + kSubs);     // four warps per scheduler: 128 registers each
 constexpr int kStages = 2;                   // key tiles and value tiles in flight
 constexpr int kInfos = 4;                    // tile descriptions in flight
 constexpr float kSlack = 8.f;                // the reference maximum may lag by 2^8 (P stays below fp16's 65504)
@@ -24,13 +23,15 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 
 struct ChunkCtrl {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_ready[2], o_done[2], drained;
+  uint64_t s_full[2], p_ready[2], o_done[2], drained[2];
   uint32_t tmem;
   int abort;
   TileInfo info[kInfos];
   float qmul[2 * kRows];                     // 2^e of each query row
   float ml[kRows][2];                        // paired streams: (m, l) of stream 1
   double freq[kHeadDim / 2];                 // RoPE pair frequencies
+  ChunkSeq sq;                               // what seldom-taken paths need of the CTA's work
+  int b, kv;
 };
 
 __host__ __device__ constexpr int chunk_smem_bytes(bool shared_keys) {
@@ -156,175 +157,207 @@ struct Work {
   int stream_tiles[2];
 };
 
-// Producer warp pw (0..3): subtiles 2 pw and 2 pw + 1 of every tile.
+// A subtile that is not a whole quantized one, both tiles; its description
+// goes into `info`.  Returns its kind.  (A function of its own with few
+// arguments: its registers are not the fast path's.)
+template <int FMT>
+__device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, int base, int quant, bool page_ok,
+                                          uint32_t kt, uint32_t vt, int sub, TileInfo& info) {
+  const kvq_cache& c = A.c;
+  const kvq_shape& s = c.shape;
+  const ChunkSeq& sq = C.sq;
+  const bool rope = s.rope_theta > 0.f;
+  const int lane = threadIdx.x & 31;
+  int ek = 0, ev = 0;
+  uint32_t bad = 0u;
+  if (!page_ok) {
+    if (lane == 0) atomicOr(c.err_word, KVQ_DEVERR_PAGE_RANGE);
+    zero_rows(kt, sub);
+    zero_rows(vt, sub);
+    bad = 1u << 16;
+  } else {
+    const size_t ring = is_token_cache(FMT) ? 0 : Addr::ring_row(s, C.b, C.kv, 0);
+    const size_t at = ((size_t)sq.t0 * s.num_kv_heads + C.kv) * kHeadDim;
+    const int64_t stride = (int64_t)s.num_kv_heads * kHeadDim;
+    const int slots = max(window_slots(s), 1);
+    const RawRows kr{(const uint16_t*)c.k_res + ring, A.k + at, stride, sq.n, sq.total, slots};
+    const RawRows vr{(const uint16_t*)c.v_res + ring, A.v + at, stride, sq.n, sq.total, slots};
+    if (quant == 0 && !rope) {
+      uint32_t none;
+      ek = rows_to_tile<true>(kr, base, kt, sub, none);
+      ev = rows_to_tile<false>(vr, base, vt, sub, bad);
+    } else {
+      TileSrc d;
+      if (quant > 0) tile_src<FMT>(c, C.b, C.kv, base / kTile, d);
+      ek = keys_any<FMT>(d, quant, kr, base, rope ? C.freq : nullptr, kt, sub);
+      ev = values_any<FMT>(d, quant, vr, base, vt, sub, bad);
+    }
+  }
+  if (ek == 0 && ev == 0 && bad == 0u) return FMT == 8 ? 1 : 0;
+  if (lane == 0) {
+    info.kmul[sub] = scale_by(1.f, ek);
+    info.vlog[sub] = (float)ev;
+    info.vinv[sub] = scale_by(1.f, -ev);
+    info.bad[sub] = bad;
+  }
+  return 2;
+}
+
+// Producer warp `sub`: subtile `sub` of every tile.  Packed words of the next
+// tile are on their way while this one's are turned into halves: the keys'
+// while the values are converted, the values' while the next keys are.
 template <int FMT, bool SHARED>
 __device__ __forceinline__ void produce(const ChunkAttnArgs& A, const Work& W, const TileRange& range, ChunkCtrl& C,
-                                        uint32_t k_tiles, uint32_t v_tiles, int pw) {
+                                        uint32_t k_tiles, uint32_t v_tiles, int sub) {
   const kvq_cache& c = A.c;
   const kvq_shape& s = c.shape;
   const ChunkSeq& sq = W.sq;
   const int lane = threadIdx.x & 31;
   const bool rope = s.rope_theta > 0.f;
   const bool direct = !rope && !s.sparse;    // whole quantized subtiles go straight from codes to halves
-  RawRows raw;
-  raw.slots = max(window_slots(s), 1);
-  raw.n = sq.n;
-  raw.total = sq.total;
-  raw.stride = (int64_t)s.num_kv_heads * kHeadDim;
-  const uint16_t* k_ring = (const uint16_t*)c.k_res + (is_token_cache(FMT) ? 0 : Addr::ring_row(s, W.b, W.kv, 0));
-  const uint16_t* v_ring = (const uint16_t*)c.v_res + (is_token_cache(FMT) ? 0 : Addr::ring_row(s, W.b, W.kv, 0));
-  const size_t at = ((size_t)sq.t0 * s.num_kv_heads + W.kv) * kHeadDim;
-  const uint16_t *k_new = A.k + at, *v_new = A.v + at;
+  UnitSrc<FMT> unit;
+  unit.init(c, W.b, W.kv);
   const int p_last = sq.n + (min(W.r0 + (SHARED ? 2 : 1) * kRows, W.rows) - 1) / W.gq;
+  SubWords<FMT> w;
 
-  for (int g = 0; g < W.tiles; ++g) {
-    const int t0 = range.tile(W.first + g) * kKeys, st = g & 1;
-    const uint32_t parity = ((g >> 1) & 1) ^ 1;
-    TileInfo& info = C.info[g % kInfos];
-    // rows outside the window may see part of the tile only
+  enum { kPacked, kOther, kBadPage };
+  struct Plan {
+    SubSrc d;
+    int base, quant, mode;
+  };
+  auto plan = [&](int g) {
+    Plan p;
+    const int t0 = range.tile(W.first + g) * kKeys;
+    p.base = t0 + kTile * sub;
+    p.quant = min(max(sq.nq - p.base, 0), kTile);
+    // rows may see part of a tile at the window's edges only
     const bool edge = A.window > 0 && t0 <= p_last - A.window && t0 + kKeys > A.sinks;
-    TileSrc d[2];
-    SubWords<FMT> w[2];
-    int mode[2];                             // 0 packed words in w, 1 bf16 rows, 2 anything, 3 none (bad page)
-    int quant[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int base = t0 + kTile * (2 * pw + i);
-      quant[i] = min(max(sq.nq - base, 0), kTile);
-      mode[i] = quant[i] == 0 ? 1 : (direct && quant[i] == kTile && !edge) ? 0 : 2;
-      if (quant[i] > 0 && !tile_src<FMT>(c, W.b, W.kv, base / kTile, d[i])) mode[i] = 3;
-      if (mode[i] == 0) load_sub<FMT>(d[i], w[i]);
-    }
-    if (!warp_wait(&C.k_empty[st], parity, &C.abort)) return;
+    p.mode = direct && p.quant == kTile && !edge ? kPacked : kOther;
+    if (p.quant > 0 && !sub_src<FMT>(unit, p.base / kTile, p.d)) p.mode = kBadPage;
+    return p;
+  };
+
+  if (W.tiles == 0) return;
+  Plan cur = plan(0);
+  if (cur.mode == kPacked) {
+    load_keys<FMT>(cur.d, w);
+    load_values<FMT>(cur.d, w);
+  }
+  for (int g = 0; g < W.tiles; ++g) {
+    const int st = g & 1;
+    const uint32_t parity = ((g >> 1) & 1) ^ 1;
     const uint32_t kt = k_tiles + st * kTileBytes16, vt = v_tiles + st * kTileBytes16;
-    // The softmax reads the description when the scores are there: it has to
-    // be complete before the keys are handed over, so value rows that need a
-    // look (raw or mixed) are written first; their stage has to be free then.
-    bool v_free = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int sub = 2 * pw + i, base = t0 + kTile * sub;
-      int ek = 0, ev = 0, kind = 0;
-      uint32_t bad = 0u;
-      if (mode[i] == 0) {
-        if (FMT == 6 && d[i].bits == 2) keys_to_tile<FMT, 2>(w[i], kt, sub);
-        else keys_to_tile<FMT, SubWords<FMT>::kBits>(w[i], kt, sub);
-      } else {
-        if (!v_free) {
-          if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
-          v_free = true;
-        }
-        kind = FMT == 8 ? 1 : 0;
-        if (mode[i] == 3) {
-          if (lane == 0) atomicOr(c.err_word, KVQ_DEVERR_PAGE_RANGE);
-          zero_rows(kt, sub);
-          zero_rows(vt, sub);
-          bad = 1u << 16;
-        } else if (mode[i] == 1 && !rope) {
-          uint32_t none;
-          raw.ring = k_ring;
-          raw.fresh = k_new;
-          ek = rows_to_tile<true>(raw, base, kt, sub, none);
-          raw.ring = v_ring;
-          raw.fresh = v_new;
-          ev = rows_to_tile<false>(raw, base, vt, sub, bad);
-        } else {
-          raw.ring = k_ring;
-          raw.fresh = k_new;
-          ek = keys_any<FMT>(d[i], quant[i], raw, base, rope ? C.freq : nullptr, kt, sub);
-          raw.ring = v_ring;
-          raw.fresh = v_new;
-          ev = values_any<FMT>(d[i], quant[i], raw, base, vt, sub, bad);
-        }
-        if (ek != 0 || ev != 0 || bad != 0u) kind = 2;
-      }
-      if (lane == 0) {
-        const bool fp8 = FMT == 8 && mode[i] == 0;
-        const float vs = fp8 ? fmaxf(d[i].vs, 0x1p-100f) : scale_by(1.f, ev);
-        info.kmul[sub] = fp8 ? d[i].ks : scale_by(1.f, ek);
-        info.vlog[sub] = fp8 ? log2f(vs) : (float)ev;
-        info.vinv[sub] = fp8 ? 1.f / vs : scale_by(1.f, -ev);
-        info.bad[sub] = bad;
-        info.kind[sub] = (uint8_t)kind;
-      }
+    TileInfo& info = C.info[g % kInfos];
+    if (!warp_wait(&C.k_empty[st], parity, &C.abort)) return;
+    int kind = 0;
+    if (cur.mode == kPacked) {
+      if (FMT == 6 && cur.d.two) keys_to_tile<FMT, 2>(w, kt, sub);
+      else keys_to_tile<FMT, SubWords<FMT>::kBits>(w, kt, sub);
+    } else {
+      // The softmax reads the description when the scores are there, so it
+      // has to be complete before the keys are handed over: rows that need a
+      // look give their values now.
+      if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
+      kind = produce_other<FMT>(A, C, cur.base, cur.quant, cur.mode != kBadPage, kt, vt, sub, info);
     }
+    if (lane == 0) info.kind[sub] = (uint8_t)kind;
     fence_async();
     __syncwarp();
     if (lane == 0) bar_arrive(&C.k_full[st]);
-    if (!v_free && !warp_wait(&C.v_empty[st], parity, &C.abort)) return;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (mode[i] != 0) continue;
-      if (FMT == 6 && d[i].bits == 2) values_to_tile<FMT, 2>(w[i], vt, 2 * pw + i);
-      else values_to_tile<FMT, SubWords<FMT>::kBits>(w[i], vt, 2 * pw + i);
+    Plan next = cur;
+    const bool more = g + 1 < W.tiles;
+    if (more) {
+      next = plan(g + 1);
+      if (next.mode == kPacked) load_keys<FMT>(next.d, w);
+    }
+    if (cur.mode == kPacked) {
+      if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
+      if (FMT == 6 && cur.d.two) values_to_tile<FMT, 2>(w, vt, sub);
+      else values_to_tile<FMT, SubWords<FMT>::kBits>(w, vt, sub);
     }
     fence_async();
     __syncwarp();
     if (lane == 0) bar_arrive(&C.v_full[st]);
+    if (more && next.mode == kPacked) load_values<FMT>(next.d, w);
+    cur = next;
   }
 }
 
-// One thread issues every product.  Streams alternate, so that one stream's
-// softmax runs while the other's products do; a stream's next scores are
-// issued behind its P V, whose P they overwrite (the tensor core takes the
-// products of one thread in order).
+// The products of stream i, issued by one thread of its first softmax warp:
+// scores of the stream's tile `it`, and its P V.  A stream's next scores
+// follow its P V, whose P they overwrite (the tensor core takes the products
+// of one thread in order); the streams alternate, so that one's softmax runs
+// while the other's products do.  False: a wait was given up.
 template <bool SHARED>
-__device__ __forceinline__ void issue(const Work& W, ChunkCtrl& C, uint32_t q_tiles, uint32_t k_tiles, uint32_t v_tiles) {
-  const uint32_t tmem = C.tmem;
-  const int streams = W.stream_tiles[1] > 0 ? 2 : 1;
-  volatile int* abort = &C.abort;
-  auto qk = [&](int i, int it) -> bool {
-    const int g = SHARED ? it : 2 * it + i, st = g & 1;
-    if (!SHARED || i == 0) {
-      if (!bar_wait(&C.k_full[st], (g >> 1) & 1, abort)) return false;
-      tc_after();
-    }
-    const uint32_t q = q_tiles + (SHARED ? i : 0) * kTileBytes16, k = k_tiles + st * kTileBytes16;
+__device__ __forceinline__ bool issue_scores(ChunkCtrl& C, int i, int it, uint32_t q_tiles, uint32_t k_tiles) {
+  const int g = SHARED ? it : 2 * it + i, st = g & 1;
+  if (!bar_wait(&C.k_full[st], (g >> 1) & 1, &C.abort)) return false;
+  tc_after();
+  const uint64_t q = operand_desc(q_tiles + (SHARED ? i : 0) * kTileBytes16, 16);
+  const uint64_t k = operand_desc(k_tiles + st * kTileBytes16, 16);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const uint32_t off = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
-      mma_ss(tm_s(tmem, i), operand_desc(q + off, 16), operand_desc(k + off, 16), kIdescQK, kk > 0);
-    }
-    if (!SHARED || i == streams - 1) tc_commit(&C.k_empty[st]);
-    tc_commit(&C.s_full[i]);
-    return true;
-  };
-  bool ok = true;
-  for (int i = 0; i < 2 && ok; ++i)
-    if (W.stream_tiles[i] > 0) ok = qk(i, 0);
-  for (int it = 0; it < W.stream_tiles[0] && ok; ++it) {
-    for (int i = 0; i < 2 && ok; ++i) {
-      if (it >= W.stream_tiles[i]) continue;
-      const int g = SHARED ? it : 2 * it + i, st = g & 1;
-      if (!(ok = bar_wait(&C.p_ready[i], it & 1, abort))) break;
-      if (!SHARED || i == 0) {
-        if (!(ok = bar_wait(&C.v_full[st], (g >> 1) & 1, abort))) break;
-      }
-      tc_after();
-      const uint32_t v = v_tiles + st * kTileBytes16;
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint64_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;     // 16 channels on
+    mma_ss(tm_s(C.tmem, i), q + off, k + off, kIdescQK, kk > 0);
+  }
+  tc_commit(&C.k_empty[st]);
+  tc_commit(&C.s_full[i]);
+  return true;
+}
+template <bool SHARED>
+__device__ __forceinline__ bool issue_values(ChunkCtrl& C, int i, int it, uint32_t v_tiles) {
+  const int g = SHARED ? it : 2 * it + i, st = g & 1;
+  if (!bar_wait(&C.p_ready[i], it & 1, &C.abort)) return false;
+  if (!bar_wait(&C.v_full[st], (g >> 1) & 1, &C.abort)) return false;
+  tc_after();
+  const uint64_t v = operand_desc(v_tiles + st * kTileBytes16, kBlockBytes);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts(tm_o(tmem, i), tm_s(tmem, i) + 8 * kk, operand_desc(v + kk * 16 * 128, kBlockBytes), kIdescPV,
-               it > 0 || kk > 0);
-      if (!SHARED || i == streams - 1) tc_commit(&C.v_empty[st]);
-      if (it + 1 < W.stream_tiles[i]) ok = qk(i, it + 1);
-      else tc_commit(&C.o_done[i]);
-    }
-  }
-  if (!ok) {                                 // given up: let the products in flight end before TMEM is freed
-    tc_commit(&C.drained);
-    const unsigned long long t0 = now_ns();
-    while (!bar_try(&C.drained, 0) && now_ns() - t0 < kWaitNs) {}
-  }
+  for (int kk = 0; kk < 8; ++kk)                           // 16 tokens on: 16 rows of 128 bytes
+    mma_ts(tm_o(C.tmem, i), tm_s(C.tmem, i) + 8 * kk, v + ((kk * 16 * 128) >> 4), kIdescPV, it > 0 || kk > 0);
+  tc_commit(&C.v_empty[st]);
+  return true;
+}
+// After a wait that was given up: the products this thread has in flight end
+// before TMEM is freed (again with a limit).
+__device__ __forceinline__ void drain(ChunkCtrl& C, int i) {
+  tc_commit(&C.drained[i]);
+  const unsigned long long t0 = now_ns();
+  while (!bar_try(&C.drained[i], 0) && now_ns() - t0 < kWaitNs) {}
 }
 
 struct RowState {
   float m, l;                                // reference (log2 units) and sum of this thread's row
 };
 
+// Packed fp32 pairs: one instruction for two numbers, each rounded on its own.
+typedef unsigned long long pair_t;
+__device__ __forceinline__ pair_t pair(float lo, float hi) {
+  pair_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(pair_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ pair_t pair_add(pair_t a, pair_t b) {
+  pair_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ pair_t pair_fma(pair_t a, pair_t b, pair_t c) {
+  pair_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The scaling of subtiles of kinds 0 and 1.
+struct Scaling {
+  float kmul, vlog, vinv;
+};
+
 // The softmax of one tile for one stream; the thread owns one row.
 template <bool SHARED>
-__device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo& info, int t0, int p_row, int p_lo,
+__device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo& info, const Scaling& packed, int t0, int p_row, int p_lo,
                                           int p_hi, float cm, bool started, uint32_t ts, uint32_t to, RowState& r) {
   const uint2 kinds = *reinterpret_cast<const uint2*>(info.kind);
   // warp-uniform: every token of the tile is visible to every row, and the whole tile has one scaling
@@ -353,7 +386,8 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
   };
   if (plain) {
     // two passes over the scores in TMEM, 64 columns in registers at a time
-    const float k = cm * info.kmul[0], vlog = info.vlog[0];
+    const bool own = (kinds.x & 0xFFu) == 0u;
+    const float k = own ? cm * packed.kmul : cm, vlog = own ? packed.vlog : 0.f;
     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int c0 = 0; c0 < kKeys; c0 += 64) {
@@ -364,12 +398,13 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
 #pragma unroll
       for (int i = 0; i < 64; i += 8) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) t4[u] = fmaxf(t4[u], fmaxf(x[i + 2 * u], x[i + 2 * u + 1]));
+        for (int u = 0; u < 4; ++u) t4[u] = fmaxf(fmaxf(t4[u], x[i + 2 * u]), x[i + 2 * u + 1]);
       }
     }
     raise(fmaf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), k, vlog));
     const float off = vlog - (r.m == -INFINITY ? 0.f : r.m);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const pair_t k2 = pair(k, k), off2 = pair(off, off);
+    pair_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
     for (int c0 = 0; c0 < kKeys; c0 += 64) {
       float x[64];
@@ -381,22 +416,32 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float a = ex2(fmaf(x[c1 + 2 * i], k, off)), b = ex2(fmaf(x[c1 + 2 * i + 1], k, off));
-          sum[(2 * i) & 3] += a;
-          sum[(2 * i + 1) & 3] += b;
+          float a, b;
+          unpair(pair_fma(pair(x[c1 + 2 * i], x[c1 + 2 * i + 1]), k2, off2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          sum[i & 1] = pair_add(sum[i & 1], pair(a, b));
           p[i] = pack_h2(a, b);
         }
         tc_st16(ts + (c0 + c1) / 2, p);
       }
     }
-    r.l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), info.vinv[0], r.l);
+    float a, b;
+    unpair(pair_add(sum[0], sum[1]), a, b);
+    r.l = fmaf(a + b, own ? packed.vinv : 1.f, r.l);
   } else {
     // subtile by subtile: its own scaling, hidden and missing tokens left out
+    auto scaling = [&](int sub) {
+      const int kind = info.kind[sub];
+      return kind == 0 ? packed : kind == 1 ? Scaling{1.f, 0.f, 1.f} : Scaling{info.kmul[sub], info.vlog[sub], info.vinv[sub]};
+    };
+    auto bad_bits = [&](int sub) { return info.kind[sub] == 2 ? info.bad[sub] : 0u; };
     auto scores = [&](int sub, float (&x)[16]) {
       tc_ld16(x, ts + kTile * sub);
       tc_wait_ld();
-      const float k = cm * info.kmul[sub], vlog = info.vlog[sub];
-      const bool none = info.bad[sub] >> 16;
+      const Scaling sc = scaling(sub);
+      const float k = cm * sc.kmul, vlog = sc.vlog;
+      const bool none = bad_bits(sub) >> 16;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const int t = t0 + kTile * sub + row_of_token(c);      // the order is its own inverse
@@ -418,7 +463,7 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
     for (int sub = 0; sub < kSubs; ++sub) {
       float x[16], sum = 0.f;
       scores(sub, x);
-      const uint32_t bad = info.bad[sub];
+      const uint32_t bad = bad_bits(sub);
       uint32_t p[8];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
@@ -429,7 +474,7 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = pack_h2(x[2 * i], x[2 * i + 1]);
       tc_st8(ts + 8 * sub, p);
-      l = fmaf(sum, info.vinv[sub], l);
+      l = fmaf(sum, scaling(sub).vinv, l);
     }
     r.l += l;
   }
@@ -477,12 +522,12 @@ __device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W,
   if (mine && partial) *reinterpret_cast<float2*>(A.ws_ml + 2 * slot) = make_float2(r.m, r.l);
 }
 
-// Grid (row blocks x splits, H_kv, B), 13 warps, one CTA per SM.
+// Grid (row blocks x splits, H_kv, B), 16 warps, one CTA per SM.
 // SHARED: 256 query rows, a stream for each half, every key tile serves both.
 // Otherwise 128 rows at most: both streams have the same rows, stream i takes
 // the tiles of parity i, and the halves of the sum are joined at the end.
 template <int FMT, bool SHARED>
-__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(ChunkAttnArgs A) {
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const __grid_constant__ ChunkAttnArgs A) {
   extern __shared__ uint8_t smem_raw[];
   grid_dependents_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -515,20 +560,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(Chunk
   uint8_t* generic = smem_raw + (q_tiles - smem_u32(smem_raw));
   ChunkCtrl& C = *reinterpret_cast<ChunkCtrl*>(generic + (v_tiles + kStages * kTileBytes16 - q_tiles));
   if (tid == 0) {
+    const int users = SHARED && W.stream_tiles[1] > 0 ? 2 : 1;     // streams that read each tile
     for (int i = 0; i < kStages; ++i) {
-      bar_init(&C.k_full[i], 4); bar_init(&C.k_empty[i], 1);
-      bar_init(&C.v_full[i], 4); bar_init(&C.v_empty[i], 1);
+      bar_init(&C.k_full[i], kSubs); bar_init(&C.k_empty[i], users);
+      bar_init(&C.v_full[i], kSubs); bar_init(&C.v_empty[i], users);
     }
-    for (int i = 0; i < 2; ++i) { bar_init(&C.s_full[i], 1); bar_init(&C.p_ready[i], 4); bar_init(&C.o_done[i], 1); }
-    bar_init(&C.drained, 1);
-    C.abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&C.s_full[i], 1); bar_init(&C.p_ready[i], 4);
+      bar_init(&C.o_done[i], 1); bar_init(&C.drained[i], 1);
+    }
+      C.abort = 0;
+    C.sq = W.sq;
+    C.b = W.b;
+    C.kv = W.kv;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == kProducerWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&C.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
-  if (s.rope_theta > 0.f && warp == kMmaWarp) {
+  if (s.rope_theta > 0.f && warp == kProducerWarp) {
     for (int i = lane; i < kHeadDim / 2; i += 32) C.freq[i] = pow((double)s.rope_theta, -2.0 * i / kHeadDim);
   }
   // Query rows -> fp16 in the key tiles' channel order, powers of two aside
@@ -538,22 +589,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(Chunk
     const uint4* src = reinterpret_cast<const uint4*>(
         A.q + ((size_t)(W.sq.t0 + R / W.gq) * s.num_q_heads + W.kv * W.gq + R % W.gq) * kHeadDim);
     float amax = 0.f;
-    uint4 w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = src[i];
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < 16; ++i) {
       float x[8];
-      unpack8(w[i], x);
+      unpack8(src[i], x);
 #pragma unroll
       for (int u = 0; u < 8; ++u) amax = fmaxf(amax, finite_abs(x[u]));
     }
     const int e = tile_exponent(amax);
     const float sign = A.scale_log2 < 0.f ? -1.f : 1.f;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < 16; ++i) {
       float x[8];
-      unpack8(w[i], x);
+      unpack8(src[i], x);
 #pragma unroll
       for (int u = 0; u < 8; ++u) x[u] = sign * (e ? scale_by(x[u], -e) : x[u]);
       put_key8(q_tiles + (tid / kRows) * kTileBytes16, tid % kRows, i, x);
@@ -566,11 +614,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(Chunk
   tc_after();
   const uint32_t tmem = C.tmem;
 
-  if (warp >= kProducerWarp && warp < kMmaWarp) {
+  if (warp >= kProducerWarp) {
     produce<FMT, SHARED>(A, W, range, C, k_tiles, v_tiles, warp - kProducerWarp);
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) issue<SHARED>(W, C, q_tiles, k_tiles, v_tiles);
-    __syncwarp();
   } else {
     const int i = warp >> 2, row = tid % kRows, R = W.r0 + (SHARED ? i * kRows : 0) + row;
     const int last = W.rows - 1;
@@ -582,22 +627,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(Chunk
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm_s(tmem, i) + lanes, to = tm_o(tmem, i) + lanes;
     RowState r{-INFINITY, 0.f};
+    Scaling packed{1.f, 0.f, 1.f};           // FP8 codes stand for themselves; the static scales come in here
+    if (FMT == 8) {
+      const float vs = fmaxf(A.c.fp8_scale[s.num_kv_heads + W.kv], 0x1p-100f);
+      packed = Scaling{A.c.fp8_scale[W.kv], log2f(vs), 1.f / vs};
+    }
+    const bool issuer = (warp & 3) == 0 && lane == 0;
     bool ok = true;
-    for (int it = 0; it < W.stream_tiles[i]; ++it) {
+    if (issuer && W.stream_tiles[i] > 0) ok = issue_scores<SHARED>(C, i, 0, q_tiles, k_tiles);
+    ok = __all_sync(0xffffffffu, ok);
+    for (int it = 0; it < W.stream_tiles[i] && ok; ++it) {
       const int g = SHARED ? it : 2 * it + i;
       if (!(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
       if (!idle) {
         tc_after();
-        soft_tile<SHARED>(A, C.info[g % kInfos], range.tile(W.first + g) * kKeys, p_row, p_lo, p_hi, cm, it > 0, ts, to,
+        soft_tile<SHARED>(A, C.info[g % kInfos], packed, range.tile(W.first + g) * kKeys, p_row, p_lo, p_hi, cm, it > 0, ts, to,
                           r);
         tc_wait_st();
         tc_before();
       }
       __syncwarp();
       if (lane == 0) bar_arrive(&C.p_ready[i]);
+      if (issuer) {
+        ok = issue_values<SHARED>(C, i, it, v_tiles);
+        if (ok && it + 1 < W.stream_tiles[i]) ok = issue_scores<SHARED>(C, i, it + 1, q_tiles, k_tiles);
+        else if (ok) tc_commit(&C.o_done[i]);
+      }
+      if ((warp & 3) == 0) ok = __all_sync(0xffffffffu, ok);
     }
     const bool any = W.stream_tiles[i] > 0;
     if (ok && any) ok = warp_wait(&C.o_done[i], 0, &C.abort);
+    if (!ok && issuer) drain(C, i);
+    __syncwarp();
     tc_after();
     const float one[2] = {1.f, 0.f};
     if (SHARED) {
@@ -635,7 +696,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(Chunk
     tc_before();
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kProducerWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
   }

@@ -108,6 +108,79 @@ __device__ __forceinline__ bool any_not_finite(const uint4& w) {
 // Whole quantized subtiles: codes -> exact halves -> one fma per pair
 // ---------------------------------------------------------------------------
 
+// The packed regions of one (sequence, kv head), for addresses of subtiles.
+template <int FMT>
+struct UnitSrc {
+  const uint8_t *k, *v;        // contiguous: the unit's first row and tile; paged: the head's part of page 0
+  const __half *km, *vm;
+  const int32_t* pages;        // paged: the sequence's table row
+  const uint8_t* widths;       // MIXED: the sequence's group widths
+  size_t page_codes, page_km, page_vm;         // paged: steps from page to page
+  int lg_group, num_pages;
+  __device__ __forceinline__ void init(const kvq_cache& c, int b, int h) {
+    const kvq_shape& s = c.shape;
+    pages = nullptr;
+    widths = nullptr;
+    lg_group = 31 - __clz(s.group | 1);
+    num_pages = s.num_pages;
+    page_codes = page_km = page_vm = 0;
+    if (s.page_size != 0) {
+      pages = c.page_table + (size_t)b * s.max_pages_per_seq;
+      page_codes = (size_t)s.num_kv_heads * tile_bytes(FMT);
+      page_km = (size_t)s.num_kv_heads * 2 * kHeadDim;
+      page_vm = (size_t)s.num_kv_heads * 2 * kTile;
+      k = (const uint8_t*)c.k_codes + Addr::pg_k_codes(s, 0, h);
+      km = (const __half*)c.k_meta + Addr::pg_k_meta(s, 0, h);
+      v = (const uint8_t*)c.v_codes + Addr::pg_v_codes(s, 0, h);
+      vm = (const __half*)c.v_meta + Addr::pg_v_meta(s, 0, h);
+      return;
+    }
+    k = (const uint8_t*)c.k_codes + Addr::k_codes_unit(s, b, h);
+    v = (const uint8_t*)c.v_codes + Addr::v_codes_tile(s, b, h, 0);
+    vm = FMT == 8 ? nullptr : (const __half*)c.v_meta + Addr::v_meta_token(s, b, h, 0);
+    km = FMT == 8 ? nullptr
+                  : (const __half*)c.k_meta + (FMT == 16 ? Addr::k_meta_token(s, b, h, 0) : Addr::k_meta_group(s, b, h, 0));
+    if (FMT == 6) widths = c.group_bits + (size_t)b * (s.capacity / s.group);
+  }
+};
+
+// Where the packed words of one subtile are.
+struct SubSrc {
+  const uint8_t *k, *v;
+  const __half *km, *vm;
+  bool two;                    // codes of 2 bits
+};
+// False if its page id is out of range.
+template <int FMT>
+__device__ __forceinline__ bool sub_src(const UnitSrc<FMT>& u, int tile, SubSrc& d) {
+  d.two = FMT == 2;
+  if (u.pages) {
+    const int page = u.pages[tile];
+    if (page < 0 || page >= u.num_pages) return false;
+    d.k = u.k + page * u.page_codes;
+    d.v = u.v + page * u.page_codes;
+    d.km = u.km + page * u.page_km;
+    d.vm = u.vm + page * u.page_vm;
+    return true;
+  }
+  d.k = u.k + (size_t)tile * tile_bytes(FMT);
+  d.v = u.v + (size_t)tile * tile_bytes(FMT);
+  d.vm = u.vm + (size_t)tile * 2 * kTile;
+  d.km = u.km;
+  if constexpr (FMT == 16) {
+    d.km = u.km + (size_t)tile * 2 * kTile;
+  } else if constexpr (FMT != 8) {
+    const int g = tile * kTile >> u.lg_group;
+    d.km = u.km + (size_t)g * 2 * kHeadDim;
+    if constexpr (FMT == 6) {
+      d.two = u.widths[g] != 4;
+      // a 2-bit group's key rows are packed from the start of its INT4 slot
+      if (d.two) d.k -= (size_t)(tile * kTile - (g << u.lg_group)) * (kHeadDim / 4);
+    }
+  }
+  return true;
+}
+
 // A subtile's packed words as one warp's lanes hold them.
 template <int FMT> struct SubWords {
   static constexpr int kBits = FMT == 6 ? 4 : (FMT == 16 ? 8 : FMT);
@@ -115,14 +188,14 @@ template <int FMT> struct SubWords {
   static constexpr int kVW = 2 * kBits;
   static constexpr int kKM = FMT == 8 ? 0 : 8;
   uint32_t k[kKW], v[kVW];
-  uint32_t km[kKM ? kKM : 1];                                // key scales and zeros (INT8: per row)
+  uint32_t km[kKM ? kKM : 1];                                // key scales, then zeros, of the lane's channels (INT8: per row)
   uint32_t vm[FMT == 8 ? 1 : 4];                             // value (scale, zero) of the lane's four tokens
 };
 
 template <int FMT>
-__device__ __forceinline__ void load_sub(const TileSrc& d, SubWords<FMT>& w) {
-  const int lane = threadIdx.x & 31, j = lane & 15, half = lane >> 4, l = lane & 3;
-  const bool two = FMT == 2 || (FMT == 6 && d.bits == 2);
+__device__ __forceinline__ void load_keys(const SubSrc& d, SubWords<FMT>& w) {
+  const int lane = threadIdx.x & 31, j = lane & 15, half = lane >> 4;
+  const bool two = FMT == 2 || (FMT == 6 && d.two);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 2 * i + half;
@@ -134,12 +207,6 @@ __device__ __forceinline__ void load_sub(const TileSrc& d, SubWords<FMT>& w) {
     } else {
       w.k[i] = *reinterpret_cast<const uint32_t*>(d.k + r * (kHeadDim / 2) + 4 * j);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < SubWords<FMT>::kVW / 4; ++i) {
-    if (FMT == 6 && two && i > 0) break;
-    const uint4 x = *reinterpret_cast<const uint4*>(d.v + 512 * i + 16 * lane);
-    w.v[4 * i] = x.x; w.v[4 * i + 1] = x.y; w.v[4 * i + 2] = x.z; w.v[4 * i + 3] = x.w;
   }
   if constexpr (FMT == 16) {
 #pragma unroll
@@ -157,10 +224,20 @@ __device__ __forceinline__ void load_sub(const TileSrc& d, SubWords<FMT>& w) {
         w.km[4 * i + 2] = prmt(a.z, b.z, sel); w.km[4 * i + 3] = prmt(a.w, b.w, sel);
       } else {
         const uint4 a = *reinterpret_cast<const uint4*>(m + 8 * j);   // pairs (0,2) (1,3) (4,6) (5,7)
-        w.km[4 * i] = prmt(a.x, a.z, 0x5410u); w.km[4 * i + 1] = prmt(a.y, a.w, 0x5410u);
-        w.km[4 * i + 2] = prmt(a.x, a.z, 0x7632u); w.km[4 * i + 3] = prmt(a.y, a.w, 0x7632u);
+        w.km[4 * i] = a.x; w.km[4 * i + 1] = a.y; w.km[4 * i + 2] = a.z; w.km[4 * i + 3] = a.w;
       }
     }
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void load_values(const SubSrc& d, SubWords<FMT>& w) {
+  const int lane = threadIdx.x & 31, l = lane & 3;
+#pragma unroll
+  for (int i = 0; i < SubWords<FMT>::kVW / 4; ++i) {
+    if (FMT == 6 && d.two && i > 0) break;
+    const uint4 x = *reinterpret_cast<const uint4*>(d.v + 512 * i + 16 * lane);
+    w.v[4 * i] = x.x; w.v[4 * i + 1] = x.y; w.v[4 * i + 2] = x.z; w.v[4 * i + 3] = x.w;
   }
   if constexpr (FMT != 8) {
 #pragma unroll
@@ -175,6 +252,19 @@ __device__ __forceinline__ void keys_to_tile(const SubWords<FMT>& w, uint32_t ti
   const int lane = threadIdx.x & 31, j = lane & 15, half = lane >> 4;
   const uint32_t base = tile + (j >> 3) * kBlockBytes + (kTile * sub + 2 * half) * 128;
   const uint32_t p = (uint32_t)((j & 7) ^ (2 * half));
+  uint32_t sc[4], zc[4];                         // scales and zeros of channels (k, k + 4)
+  if constexpr (FMT != 8 && FMT != 16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (BITS == 2) {
+        sc[k] = w.km[k];
+        zc[k] = w.km[4 + k];
+      } else {
+        sc[k] = prmt(w.km[k & 1], w.km[2 + (k & 1)], k < 2 ? 0x5410u : 0x7632u);
+        zc[k] = prmt(w.km[4 + (k & 1)], w.km[6 + (k & 1)], k < 2 ? 0x5410u : 0x7632u);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {                  // token row 2i + half -> tile row 4 (i / 2) + 2 half + i % 2
     const uint32_t at = base + (4 * (i >> 1) + (i & 1)) * 128 + ((p ^ (4 * ((i >> 1) & 1) + (i & 1))) << 4);
@@ -204,7 +294,7 @@ __device__ __forceinline__ void keys_to_tile(const SubWords<FMT>& w, uint32_t ti
       for (int k = 0; k < 4; ++k) x[k] = f16_fma(x[k], s, z);
     } else if constexpr (FMT != 8) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = f16_fma(x[k], w.km[k], w.km[4 + k]);
+      for (int k = 0; k < 4; ++k) x[k] = f16_fma(x[k], sc[k], zc[k]);
     }
     st_shared16(at, x[0], x[1], x[2], x[3]);
   }
@@ -313,7 +403,7 @@ __device__ __forceinline__ void rope8(float (&x)[8], int t, int ch, const double
 // packed tile d, the others raw.  Two passes (largest magnitude, then the
 // rows), so that any range of numbers fits.  Returns the power of two taken out.
 template <int FMT>
-__device__ __noinline__ int keys_any(const TileSrc& d, int quant, const RawRows& raw, int base, const double* freq,
+__device__ __forceinline__ int keys_any(const TileSrc& d, int quant, const RawRows& raw, int base, const double* freq,
                                      uint32_t tile, int sub) {
   const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
   float amax = 0.f;
@@ -349,7 +439,7 @@ __device__ __noinline__ int keys_any(const TileSrc& d, int quant, const RawRows&
 // Values alike; rows with a value that is not finite become zero and set
 // their tile row's bit in `bad`.
 template <int FMT>
-__device__ __noinline__ int values_any(const TileSrc& d, int quant, const RawRows& raw, int base, uint32_t tile, int sub,
+__device__ __forceinline__ int values_any(const TileSrc& d, int quant, const RawRows& raw, int base, uint32_t tile, int sub,
                                        uint32_t& bad) {
   const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
   float amax = 0.f;
