@@ -21,17 +21,24 @@ constexpr int kInfos = 4;                    // tile descriptions in flight
 constexpr float kSlack = 8.f;                // the reference maximum may lag by 2^8 (P stays below fp16's 65504)
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
+// What every thread of a CTA knows about its work.
+struct Work {
+  ChunkSeq sq;
+  int b, kv, gq, r0, rows, split;
+  int first, tiles;                          // tiles [first, first + tiles) of the range
+  int stream_tiles[2];
+};
+
 struct ChunkCtrl {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_ready[2], o_done[2], drained[2];
+  uint64_t s_full[2], p_ready[2], o_done[2], turn[2], drained[2];
   uint32_t tmem;
   int abort;
   TileInfo info[kInfos];
   float qmul[2 * kRows];                     // 2^e of each query row
   float ml[kRows][2];                        // paired streams: (m, l) of stream 1
   double freq[kHeadDim / 2];                 // RoPE pair frequencies
-  ChunkSeq sq;                               // what seldom-taken paths need of the CTA's work
-  int b, kv;
+  Work work;                                 // kept here, not in every thread's registers
 };
 
 __host__ __device__ constexpr int chunk_smem_bytes(bool shared_keys) {
@@ -76,6 +83,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
+}
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
@@ -143,19 +156,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// TMEM columns: S of the streams (P over it), then O of the streams.
+// TMEM columns: S of the streams (P over the second half of it), then O of the streams.
+constexpr int kPColumn = 64;
 __device__ __forceinline__ uint32_t tm_s(uint32_t tmem, int i) { return tmem + 128 * i; }
 __device__ __forceinline__ uint32_t tm_o(uint32_t tmem, int i) { return tmem + 256 + 128 * i; }
 
 // --- the kernel -----------------------------------------------------------
-
-// What every thread of a CTA knows about its work.
-struct Work {
-  ChunkSeq sq;
-  int b, kv, gq, r0, rows, split;
-  int first, tiles;                          // tiles [first, first + tiles) of the range
-  int stream_tiles[2];
-};
 
 // A subtile that is not a whole quantized one, both tiles; its description
 // goes into `info`.  Returns its kind.  (A function of its own with few
@@ -165,7 +171,7 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
                                           uint32_t kt, uint32_t vt, int sub, TileInfo& info) {
   const kvq_cache& c = A.c;
   const kvq_shape& s = c.shape;
-  const ChunkSeq& sq = C.sq;
+  const ChunkSeq& sq = C.work.sq;
   const bool rope = s.rope_theta > 0.f;
   const int lane = threadIdx.x & 31;
   int ek = 0, ev = 0;
@@ -176,8 +182,8 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
     zero_rows(vt, sub);
     bad = 1u << 16;
   } else {
-    const size_t ring = is_token_cache(FMT) ? 0 : Addr::ring_row(s, C.b, C.kv, 0);
-    const size_t at = ((size_t)sq.t0 * s.num_kv_heads + C.kv) * kHeadDim;
+    const size_t ring = is_token_cache(FMT) ? 0 : Addr::ring_row(s, C.work.b, C.work.kv, 0);
+    const size_t at = ((size_t)sq.t0 * s.num_kv_heads + C.work.kv) * kHeadDim;
     const int64_t stride = (int64_t)s.num_kv_heads * kHeadDim;
     const int slots = max(window_slots(s), 1);
     const RawRows kr{(const uint16_t*)c.k_res + ring, A.k + at, stride, sq.n, sq.total, slots};
@@ -188,7 +194,7 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       ev = rows_to_tile<false>(vr, base, vt, sub, bad);
     } else {
       TileSrc d;
-      if (quant > 0) tile_src<FMT>(c, C.b, C.kv, base / kTile, d);
+      if (quant > 0) tile_src<FMT>(c, C.work.b, C.work.kv, base / kTile, d);
       ek = keys_any<FMT>(d, quant, kr, base, rope ? C.freq : nullptr, kt, sub);
       ev = values_any<FMT>(d, quant, vr, base, vt, sub, bad);
     }
@@ -207,114 +213,125 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
 // tile are on their way while this one's are turned into halves: the keys'
 // while the values are converted, the values' while the next keys are.
 template <int FMT, bool SHARED>
-__device__ __forceinline__ void produce(const ChunkAttnArgs& A, const Work& W, const TileRange& range, ChunkCtrl& C,
+__device__ __forceinline__ void produce(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C, UnitSrc<FMT>& unit,
                                         uint32_t k_tiles, uint32_t v_tiles, int sub) {
-  const kvq_cache& c = A.c;
-  const kvq_shape& s = c.shape;
-  const ChunkSeq& sq = W.sq;
   const int lane = threadIdx.x & 31;
-  const bool rope = s.rope_theta > 0.f;
-  const bool direct = !rope && !s.sparse;    // whole quantized subtiles go straight from codes to halves
-  UnitSrc<FMT> unit;
-  unit.init(c, W.b, W.kv);
-  const int p_last = sq.n + (min(W.r0 + (SHARED ? 2 : 1) * kRows, W.rows) - 1) / W.gq;
+  const int first = C.work.first, tiles = C.work.tiles, nq = C.work.sq.nq;
+  const bool direct = A.c.shape.rope_theta <= 0.f && !A.c.shape.sparse;   // codes straight to halves
+  const int p_last = C.work.sq.n + (min(C.work.r0 + (SHARED ? 2 : 1) * kRows, C.work.rows) - 1) / C.work.gq;
   SubWords<FMT> w;
+  SubSrc d;
 
   enum { kPacked, kOther, kBadPage };
   struct Plan {
-    SubSrc d;
-    int base, quant, mode;
+    int base, mode;
+    bool two;
   };
   auto plan = [&](int g) {
     Plan p;
-    const int t0 = range.tile(W.first + g) * kKeys;
+    const int t0 = range.tile(first + g) * kKeys;
     p.base = t0 + kTile * sub;
-    p.quant = min(max(sq.nq - p.base, 0), kTile);
     // rows may see part of a tile at the window's edges only
     const bool edge = A.window > 0 && t0 <= p_last - A.window && t0 + kKeys > A.sinks;
-    p.mode = direct && p.quant == kTile && !edge ? kPacked : kOther;
-    if (p.quant > 0 && !sub_src<FMT>(unit, p.base / kTile, p.d)) p.mode = kBadPage;
+    p.mode = direct && nq - p.base >= kTile && !edge ? kPacked : kOther;
+    if (nq > p.base && !sub_src<FMT>(unit, p.base / kTile, d)) p.mode = kBadPage;
+    p.two = FMT == 2 || (FMT == 6 && d.two);
     return p;
   };
 
-  if (W.tiles == 0) return;
+  if (tiles == 0) return;
   Plan cur = plan(0);
   if (cur.mode == kPacked) {
-    load_keys<FMT>(cur.d, w);
-    load_values<FMT>(cur.d, w);
+    load_keys<FMT>(d, w);
+    load_values<FMT>(d, w);
   }
-  for (int g = 0; g < W.tiles; ++g) {
+  for (int g = 0; g < tiles; ++g) {
     const int st = g & 1;
     const uint32_t parity = ((g >> 1) & 1) ^ 1;
     const uint32_t kt = k_tiles + st * kTileBytes16, vt = v_tiles + st * kTileBytes16;
-    TileInfo& info = C.info[g % kInfos];
     if (!warp_wait(&C.k_empty[st], parity, &C.abort)) return;
     int kind = 0;
     if (cur.mode == kPacked) {
-      if (FMT == 6 && cur.d.two) keys_to_tile<FMT, 2>(w, kt, sub);
+      if (FMT == 6 && cur.two) keys_to_tile<FMT, 2>(w, kt, sub);
       else keys_to_tile<FMT, SubWords<FMT>::kBits>(w, kt, sub);
     } else {
       // The softmax reads the description when the scores are there, so it
       // has to be complete before the keys are handed over: rows that need a
       // look give their values now.
       if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
-      kind = produce_other<FMT>(A, C, cur.base, cur.quant, cur.mode != kBadPage, kt, vt, sub, info);
+      kind = produce_other<FMT>(A, C, cur.base, min(max(nq - cur.base, 0), kTile), cur.mode != kBadPage, kt, vt, sub,
+                                C.info[g % kInfos]);
+      w = SubWords<FMT>{};                   // nothing to keep over the call
     }
-    if (lane == 0) info.kind[sub] = (uint8_t)kind;
+    if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
     fence_async();
     __syncwarp();
     if (lane == 0) bar_arrive(&C.k_full[st]);
     Plan next = cur;
-    const bool more = g + 1 < W.tiles;
+    const bool more = g + 1 < tiles;
     if (more) {
       next = plan(g + 1);
-      if (next.mode == kPacked) load_keys<FMT>(next.d, w);
+      if (next.mode == kPacked) load_keys<FMT>(d, w);
     }
     if (cur.mode == kPacked) {
       if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
-      if (FMT == 6 && cur.d.two) values_to_tile<FMT, 2>(w, vt, sub);
+      if (FMT == 6 && cur.two) values_to_tile<FMT, 2>(w, vt, sub);
       else values_to_tile<FMT, SubWords<FMT>::kBits>(w, vt, sub);
     }
     fence_async();
     __syncwarp();
     if (lane == 0) bar_arrive(&C.v_full[st]);
-    if (more && next.mode == kPacked) load_values<FMT>(next.d, w);
+    if (more && next.mode == kPacked) load_values<FMT>(d, w);
     cur = next;
   }
 }
 
-// The products of stream i, issued by one thread of its first softmax warp:
+// The products of stream i, issued by the first warp of its softmax (the whole
+// warp waits, one elected thread issues; descriptors are warp-uniform):
 // scores of the stream's tile `it`, and its P V.  A stream's next scores
 // follow its P V, whose P they overwrite (the tensor core takes the products
 // of one thread in order); the streams alternate, so that one's softmax runs
 // while the other's products do.  False: a wait was given up.
+struct Products {
+  uint64_t q, k, v;            // operand descriptors: the stream's rows, stage 0 of the keys and of the values
+  uint32_t s, o;               // TMEM columns of the stream's scores (P in their second half) and output
+};
+constexpr uint32_t kStageStep = kTileBytes16 >> 4;
+
 template <bool SHARED>
-__device__ __forceinline__ bool issue_scores(ChunkCtrl& C, int i, int it, uint32_t q_tiles, uint32_t k_tiles) {
+__device__ __forceinline__ bool issue_scores(ChunkCtrl& C, const Products& P, int i, int it) {
   const int g = SHARED ? it : 2 * it + i, st = g & 1;
-  if (!bar_wait(&C.k_full[st], (g >> 1) & 1, &C.abort)) return false;
+  if (!warp_wait(&C.k_full[st], (g >> 1) & 1, &C.abort)) return false;
   tc_after();
-  const uint64_t q = operand_desc(q_tiles + (SHARED ? i : 0) * kTileBytes16, 16);
-  const uint64_t k = operand_desc(k_tiles + st * kTileBytes16, 16);
+  const uint64_t k = P.k + st * kStageStep;
+  if (elect_one()) {
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint64_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;     // 16 channels on
-    mma_ss(tm_s(C.tmem, i), q + off, k + off, kIdescQK, kk > 0);
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint64_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;   // 16 channels on
+      mma_ss(P.s, P.q + off, k + off, kIdescQK, kk > 0);
+    }
+    tc_commit(&C.k_empty[st]);
+    tc_commit(&C.s_full[i]);
   }
-  tc_commit(&C.k_empty[st]);
-  tc_commit(&C.s_full[i]);
+  __syncwarp();
   return true;
 }
 template <bool SHARED>
-__device__ __forceinline__ bool issue_values(ChunkCtrl& C, int i, int it, uint32_t v_tiles) {
+__device__ __forceinline__ bool issue_values(ChunkCtrl& C, const Products& P, int i, int it, bool last) {
   const int g = SHARED ? it : 2 * it + i, st = g & 1;
-  if (!bar_wait(&C.p_ready[i], it & 1, &C.abort)) return false;
-  if (!bar_wait(&C.v_full[st], (g >> 1) & 1, &C.abort)) return false;
+  if (!warp_wait(&C.p_ready[i], it & 1, &C.abort)) return false;
+  if (!warp_wait(&C.v_full[st], (g >> 1) & 1, &C.abort)) return false;
   tc_after();
-  const uint64_t v = operand_desc(v_tiles + st * kTileBytes16, kBlockBytes);
+  const uint64_t v = P.v + st * kStageStep;
+  const uint32_t add = it > 0;
+  if (elect_one()) {
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)                           // 16 tokens on: 16 rows of 128 bytes
-    mma_ts(tm_o(C.tmem, i), tm_s(C.tmem, i) + 8 * kk, v + ((kk * 16 * 128) >> 4), kIdescPV, it > 0 || kk > 0);
-  tc_commit(&C.v_empty[st]);
+    for (int kk = 0; kk < 8; ++kk)                         // 16 tokens on: 16 rows of 128 bytes
+      mma_ts(P.o, P.s + kPColumn + 8 * kk, v + ((kk * 16 * 128) >> 4), kIdescPV, kk > 0 ? 1u : add);
+    tc_commit(&C.v_empty[st]);
+    if (last) tc_commit(&C.o_done[i]);
+  }
+  __syncwarp();
   return true;
 }
 // After a wait that was given up: the products this thread has in flight end
@@ -385,11 +402,11 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
     r.m = mn;
   };
   if (plain) {
-    // two passes over the scores in TMEM, 64 columns in registers at a time
+    // two passes over the scores in TMEM: a row does not fit the registers
     const bool own = (kinds.x & 0xFFu) == 0u;
     const float k = own ? cm * packed.kmul : cm, vlog = own ? packed.vlog : 0.f;
     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
     for (int c0 = 0; c0 < kKeys; c0 += 64) {
       float x[64];
       tc_ld32(x, ts + c0);
@@ -405,8 +422,9 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
     const float off = vlog - (r.m == -INFINITY ? 0.f : r.m);
     const pair_t k2 = pair(k, k), off2 = pair(off, off);
     pair_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-    for (int c0 = 0; c0 < kKeys; c0 += 64) {
+    // from the upper half down: P lies over scores that have been read
+#pragma unroll 1
+    for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {
       float x[64];
       tc_ld32(x, ts + c0);
       tc_ld32(x + 32, ts + c0 + 32);
@@ -423,7 +441,7 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
           sum[i & 1] = pair_add(sum[i & 1], pair(a, b));
           p[i] = pack_h2(a, b);
         }
-        tc_st16(ts + (c0 + c1) / 2, p);
+        tc_st16(ts + kPColumn + (c0 + c1) / 2, p);
       }
     }
     float a, b;
@@ -460,7 +478,7 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
     const float ref = r.m == -INFINITY ? 0.f : r.m;
     float l = 0.f;
 #pragma unroll 1
-    for (int sub = 0; sub < kSubs; ++sub) {
+    for (int sub = kSubs - 1; sub >= 0; --sub) {             // downwards: see above
       float x[16], sum = 0.f;
       scores(sub, x);
       const uint32_t bad = bad_bits(sub);
@@ -473,7 +491,7 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = pack_h2(x[2 * i], x[2 * i + 1]);
-      tc_st8(ts + 8 * sub, p);
+      tc_st8(ts + kPColumn + 8 * sub, p);
       l = fmaf(sum, scaling(sub).vinv, l);
     }
     r.l += l;
@@ -522,6 +540,106 @@ __device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W,
   if (mine && partial) *reinterpret_cast<float2*>(A.ws_ml + 2 * slot) = make_float2(r.m, r.l);
 }
 
+// The softmax of stream i; this thread has row `row` of the stream's rows.
+template <int FMT, bool SHARED>
+__device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C, uint32_t q_tiles,
+                                       uint32_t k_tiles, uint32_t v_tiles, int i, int row, uint8_t* generic) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Work& W = C.work;
+  const int tiles = W.stream_tiles[i], other_tiles = W.stream_tiles[1 - i];
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+  const uint32_t ts = tm_s(C.tmem, i) + lanes, to = tm_o(C.tmem, i) + lanes;
+  const int R = W.r0 + (SHARED ? i * kRows : 0) + row;
+  const bool idle = R - lane >= W.rows;                      // no row of this warp is real
+  RowState r{-INFINITY, 0.f};
+  const bool issuer = (warp & 3) == 0;                       // this warp issues the stream's products
+  bool ok = true;
+  Products P;
+  {
+    const uint32_t tmem = __shfl_sync(0xffffffffu, C.tmem, 0);
+    P.q = operand_desc(q_tiles + (SHARED ? i : 0) * kTileBytes16, 16);
+    P.k = operand_desc(k_tiles, 16);
+    P.v = operand_desc(v_tiles, kBlockBytes);
+    P.s = tm_s(tmem, i);
+    P.o = tm_o(tmem, i);
+  }
+  {
+    const int last = W.rows - 1, n = W.sq.n, w0 = R - lane;
+    const int p_row = n + min(R, last) / W.gq;
+    const int p_lo = n + min(w0, last) / W.gq, p_hi = n + min(w0 + 31, last) / W.gq;
+    const float cm = fabsf(A.scale_log2) * C.qmul[SHARED ? i * kRows + row : row];
+    Scaling packed{1.f, 0.f, 1.f};           // FP8 codes stand for themselves; the static scales come in here
+    if (FMT == 8) {
+      const float vs = fmaxf(A.c.fp8_scale[A.c.shape.num_kv_heads + W.kv], 0x1p-100f);
+      packed = Scaling{A.c.fp8_scale[W.kv], log2f(vs), 1.f / vs};
+    }
+    const int first = W.first;
+    if (issuer && tiles > 0) ok = issue_scores<SHARED>(C, P, i, 0);
+    for (int it = 0; it < tiles && ok; ++it) {
+      const int g = SHARED ? it : 2 * it + i;
+      if (!(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
+      if (!idle) {
+        tc_after();
+        soft_tile<SHARED>(A, C.info[g % kInfos], packed, range.tile(first + g) * kKeys, p_row, p_lo, p_hi, cm, it > 0, ts,
+                          to, r);
+        tc_wait_st();
+        tc_before();
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(&C.p_ready[i]);
+      if (issuer) {
+        // The streams take turns at the tensor cores, a stream's P V and next
+        // scores together: left to themselves both would compute and both
+        // would multiply at the same time.
+        if (i == 0) ok = it == 0 || it > other_tiles || warp_wait(&C.turn[0], (it - 1) & 1, &C.abort);
+        else ok = warp_wait(&C.turn[1], it & 1, &C.abort);
+        ok = ok && issue_values<SHARED>(C, P, i, it, it + 1 == tiles);
+        if (ok && it + 1 < tiles) ok = issue_scores<SHARED>(C, P, i, it + 1);
+        if (lane == 0) bar_arrive(&C.turn[1 - i]);
+      }
+    }
+  }
+  const bool any = tiles > 0;
+  if (ok && any) ok = warp_wait(&C.o_done[i], 0, &C.abort);
+  if (!ok && issuer && elect_one()) drain(C, i);
+  __syncwarp();
+  tc_after();
+  const float one[2] = {1.f, 0.f};
+  if (SHARED) {
+    if (ok && !idle) store_row(A, W, R, r, to, any, nullptr, one);
+  } else {
+    // join the streams: stream 1's row through shared memory (the tiles are used up)
+    float* o1 = reinterpret_cast<float*>(generic + kTileBytes16) + row * kHeadDim;
+    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    if (i == 1) {
+      C.ml[row][0] = r.m;
+      C.ml[row][1] = r.l;
+      if (ok && any && !idle) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+          float o[32];
+          tc_ld32(o, to + c0);
+          tc_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<float4*>(o1 + 4 * ((c0 / 4 + u) ^ lane)) =
+                make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        }
+      }
+    }
+    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    if (i == 0 && ok && !idle) {
+      const float m1 = C.ml[row][0], l1 = C.ml[row][1];
+      const bool two = other_tiles > 0;
+      const float M = fmaxf(r.m, m1), ref = M == -INFINITY ? 0.f : M;
+      const float f[2] = {ex2(r.m - ref), two && m1 != -INFINITY ? ex2(m1 - ref) : 0.f};
+      const RowState j{M, r.l * f[0] + (two ? l1 * f[1] : 0.f)};
+      store_row(A, W, R, j, to, any, two ? o1 : nullptr, f);
+    }
+  }
+  tc_before();
+}
+
 // Grid (row blocks x splits, H_kv, B), 16 warps, one CTA per SM.
 // SHARED: 256 query rows, a stream for each half, every key tile serves both.
 // Otherwise 128 rows at most: both streams have the same rows, stream i takes
@@ -567,18 +685,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&C.s_full[i], 1); bar_init(&C.p_ready[i], 4);
-      bar_init(&C.o_done[i], 1); bar_init(&C.drained[i], 1);
+      bar_init(&C.o_done[i], 1); bar_init(&C.turn[i], 1); bar_init(&C.drained[i], 1);
     }
       C.abort = 0;
-    C.sq = W.sq;
-    C.b = W.b;
-    C.kv = W.kv;
+    C.work = W;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kProducerWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&C.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
+  __shared__ UnitSrc<FMT> unit;              // read again for every tile: no registers held
+  if (tid == 32 * kProducerWarp) unit.init(A.c, W.b, W.kv);
   if (s.rope_theta > 0.f && warp == kProducerWarp) {
     for (int i = lane; i < kHeadDim / 2; i += 32) C.freq[i] = pow((double)s.rope_theta, -2.0 * i / kHeadDim);
   }
@@ -615,85 +733,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
   const uint32_t tmem = C.tmem;
 
   if (warp >= kProducerWarp) {
-    produce<FMT, SHARED>(A, W, range, C, k_tiles, v_tiles, warp - kProducerWarp);
+    produce<FMT, SHARED>(A, range, C, unit, k_tiles, v_tiles, warp - kProducerWarp);
   } else {
-    const int i = warp >> 2, row = tid % kRows, R = W.r0 + (SHARED ? i * kRows : 0) + row;
-    const int last = W.rows - 1;
-    const int w0 = W.r0 + (SHARED ? i * kRows : 0) + 32 * (warp & 3);      // the warp's first row
-    const bool idle = w0 > last;
-    const int p_row = W.sq.n + min(R, last) / W.gq;
-    const int p_lo = W.sq.n + min(w0, last) / W.gq, p_hi = W.sq.n + min(w0 + 31, last) / W.gq;
-    const float cm = fabsf(A.scale_log2) * C.qmul[SHARED ? tid : row];
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tm_s(tmem, i) + lanes, to = tm_o(tmem, i) + lanes;
-    RowState r{-INFINITY, 0.f};
-    Scaling packed{1.f, 0.f, 1.f};           // FP8 codes stand for themselves; the static scales come in here
-    if (FMT == 8) {
-      const float vs = fmaxf(A.c.fp8_scale[s.num_kv_heads + W.kv], 0x1p-100f);
-      packed = Scaling{A.c.fp8_scale[W.kv], log2f(vs), 1.f / vs};
-    }
-    const bool issuer = (warp & 3) == 0 && lane == 0;
-    bool ok = true;
-    if (issuer && W.stream_tiles[i] > 0) ok = issue_scores<SHARED>(C, i, 0, q_tiles, k_tiles);
-    ok = __all_sync(0xffffffffu, ok);
-    for (int it = 0; it < W.stream_tiles[i] && ok; ++it) {
-      const int g = SHARED ? it : 2 * it + i;
-      if (!(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
-      if (!idle) {
-        tc_after();
-        soft_tile<SHARED>(A, C.info[g % kInfos], packed, range.tile(W.first + g) * kKeys, p_row, p_lo, p_hi, cm, it > 0, ts, to,
-                          r);
-        tc_wait_st();
-        tc_before();
-      }
-      __syncwarp();
-      if (lane == 0) bar_arrive(&C.p_ready[i]);
-      if (issuer) {
-        ok = issue_values<SHARED>(C, i, it, v_tiles);
-        if (ok && it + 1 < W.stream_tiles[i]) ok = issue_scores<SHARED>(C, i, it + 1, q_tiles, k_tiles);
-        else if (ok) tc_commit(&C.o_done[i]);
-      }
-      if ((warp & 3) == 0) ok = __all_sync(0xffffffffu, ok);
-    }
-    const bool any = W.stream_tiles[i] > 0;
-    if (ok && any) ok = warp_wait(&C.o_done[i], 0, &C.abort);
-    if (!ok && issuer) drain(C, i);
-    __syncwarp();
-    tc_after();
-    const float one[2] = {1.f, 0.f};
-    if (SHARED) {
-      if (ok && !idle) store_row(A, W, R, r, to, any, nullptr, one);
-    } else {
-      // join the streams: stream 1's row through shared memory (the tiles are used up)
-      float* o1 = reinterpret_cast<float*>(generic + kTileBytes16) + row * kHeadDim;
-      asm volatile("bar.sync 1, 256;\n" ::: "memory");
-      if (i == 1) {
-        C.ml[row][0] = r.m;
-        C.ml[row][1] = r.l;
-        if (ok && any && !idle) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
-            float o[32];
-            tc_ld32(o, to + c0);
-            tc_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<float4*>(o1 + 4 * ((c0 / 4 + u) ^ lane)) =
-                  make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-          }
-        }
-      }
-      asm volatile("bar.sync 1, 256;\n" ::: "memory");
-      if (i == 0 && ok && !idle) {
-        const float m1 = C.ml[row][0], l1 = C.ml[row][1];
-        const bool two = W.stream_tiles[1] > 0;
-        const float M = fmaxf(r.m, m1), ref = M == -INFINITY ? 0.f : M;
-        const float f[2] = {ex2(r.m - ref), two && m1 != -INFINITY ? ex2(m1 - ref) : 0.f};
-        RowState j{M, r.l * f[0] + (two ? l1 * f[1] : 0.f)};
-        store_row(A, W, R, j, to, any, two ? o1 : nullptr, f);
-      }
-    }
-    tc_before();
+    const int i = __shfl_sync(0xffffffffu, warp >> 2, 0), row = tid % kRows;   // warp-uniform for the compiler too
+    soften<FMT, SHARED>(A, range, C, q_tiles, k_tiles, v_tiles, i, row, generic);
   }
   __syncthreads();
   if (warp == kProducerWarp) {
