@@ -4,8 +4,8 @@
 // Per (sequence, kv head) the query rows of all gq heads and new tokens form
 // one matrix (row R = head R % gq of token R / gq).  For each tile of 128
 // tokens: S = Q K^T (128 rows x 128 keys, fp16 operands, fp32 in TMEM), the
-// online softmax with one thread per row, P = fp16 back into TMEM, O += P V
-// with O in TMEM.  Packed tokens become fp16 operands once per CTA and tile
+// online softmax with one thread per row (64 keys at a time), P = fp16 back
+// into TMEM, O += P V with O in TMEM.  Packed tokens become fp16 operands once per CTA and tile
 // (kvq_tiles.cuh); fp16 holds every code exactly and a dequantized number to
 // 2^-11, eight times finer than bf16, and powers of two are taken out of raw
 // rows that would not fit.
@@ -14,9 +14,19 @@
 namespace kvq {
 
 constexpr int kRows = 128;                   // query rows per stream: one TMEM lane and one softmax thread each
-constexpr int kProducerWarp = 8;             // warps 0-3 and 4-7: softmax of streams 0 and 1; 8-15: producers
-constexpr int kChunkThreads = 32 * (kProducerWarp + kSubs);     // four warps per scheduler: 128 registers each
-constexpr int kStages = 2;                   // key tiles and value tiles in flight
+constexpr int kProducerWarp = 8;             // warps 0-3 and 4-7: softmax of streams 0 and 1; 8-14: producers
+constexpr int kProducers = 7;
+constexpr int kMmaWarp = kProducerWarp + kProducers;            // issues every product
+constexpr int kChunkThreads = 32 * (kMmaWarp + 1);              // four warps per scheduler: 128 registers each
+constexpr int kHalf = kKeys / 2;             // keys per score block: each stream has two
+constexpr int kStages = 2;                   // key tiles in flight
+// Value tiles in flight.  A producer may have two subtiles of one tile, and
+// writes the values of the first before the keys of the second.  Paired
+// streams ask for the keys of tile g + 2 while the values of tile g are still
+// in use (and those of tile g - 1 are used up): the values of tile g + 2 need
+// a third stage.  Shared keys: those of tile g + 1 while g - 1 is used up.
+__host__ __device__ constexpr int value_stages(bool shared_keys) { return shared_keys ? 2 : 3; }
+constexpr int kMaxValueStages = 3;
 constexpr int kInfos = 4;                    // tile descriptions in flight
 constexpr float kSlack = 8.f;                // the reference maximum may lag by 2^8 (P stays below fp16's 65504)
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -30,8 +40,8 @@ struct Work {
 };
 
 struct ChunkCtrl {
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_ready[2], o_done[2], turn[2], drained[2];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kMaxValueStages], v_empty[kMaxValueStages];
+  uint64_t s_full[2][2], p_ready[2][2], o_done[2], drained;   // [stream][half of the tile]
   uint32_t tmem;
   int abort;
   TileInfo info[kInfos];
@@ -42,7 +52,7 @@ struct ChunkCtrl {
 };
 
 __host__ __device__ constexpr int chunk_smem_bytes(bool shared_keys) {
-  return 1024 + (shared_keys ? 2 : 1) * kTileBytes16 + 2 * kStages * kTileBytes16 + (int)sizeof(ChunkCtrl);
+  return 1024 + ((shared_keys ? 2 : 1) + kStages + value_stages(shared_keys)) * kTileBytes16 + (int)sizeof(ChunkCtrl);
 }
 
 // --- mbarriers, tcgen05 ---------------------------------------------------
@@ -139,9 +149,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-// fp16 x fp16 -> fp32, M = N = 128; the value operand is stored with channels (N) contiguous.
-constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
-constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+// fp16 x fp16 -> fp32, M = 128; N = 64 keys, or 128 channels (stored with channels contiguous).
+constexpr uint32_t kIdescQK = (1u << 4) | ((kHalf / 8) << 17) | (8u << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (16u << 17) | (8u << 24) | (1u << 16);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
@@ -156,8 +166,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// TMEM columns: S of the streams (P over the second half of it), then O of the streams.
-constexpr int kPColumn = 64;
+// TMEM columns: S of the streams, half by half (P over the start of its half), then O of the streams.
 __device__ __forceinline__ uint32_t tm_s(uint32_t tmem, int i) { return tmem + 128 * i; }
 __device__ __forceinline__ uint32_t tm_o(uint32_t tmem, int i) { return tmem + 256 + 128 * i; }
 
@@ -167,16 +176,18 @@ __device__ __forceinline__ uint32_t tm_o(uint32_t tmem, int i) { return tmem + 2
 // goes into `info`.  Returns its kind.  (A function of its own with few
 // arguments: its registers are not the fast path's.)
 template <int FMT>
-__device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, int base, int quant, bool page_ok,
-                                          uint32_t kt, uint32_t vt, int sub, TileInfo& info) {
+__device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, int base, uint32_t kt, uint32_t vt,
+                                          int sub, TileInfo& info) {
   const kvq_cache& c = A.c;
   const kvq_shape& s = c.shape;
   const ChunkSeq& sq = C.work.sq;
   const bool rope = s.rope_theta > 0.f;
   const int lane = threadIdx.x & 31;
+  const int quant = min(max(sq.nq - base, 0), kTile);        // quantized rows come first
   int ek = 0, ev = 0;
   uint32_t bad = 0u;
-  if (!page_ok) {
+  TileSrc d;
+  if (quant > 0 && !tile_src<FMT>(c, C.work.b, C.work.kv, base / kTile, d)) {
     if (lane == 0) atomicOr(c.err_word, KVQ_DEVERR_PAGE_RANGE);
     zero_rows(kt, sub);
     zero_rows(vt, sub);
@@ -193,8 +204,6 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       ek = rows_to_tile<true>(kr, base, kt, sub, none);
       ev = rows_to_tile<false>(vr, base, vt, sub, bad);
     } else {
-      TileSrc d;
-      if (quant > 0) tile_src<FMT>(c, C.work.b, C.work.kv, base / kTile, d);
       ek = keys_any<FMT>(d, quant, kr, base, rope ? C.freq : nullptr, kt, sub);
       ev = values_any<FMT>(d, quant, vr, base, vt, sub, bad);
     }
@@ -209,137 +218,178 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
   return 2;
 }
 
-// Producer warp `sub`: subtile `sub` of every tile.  Packed words of the next
-// tile are on their way while this one's are turned into halves: the keys'
-// while the values are converted, the values' while the next keys are.
+// Producer warp pw: every seventh subtile (subtile x is number x % 8 of tile
+// x / 8).  In a run of whole quantized subtiles the keys are one subtile ahead
+// of the values, K(x) K(x + 7) V(x) K(x + 14) V(x + 7) ..., so that a tile's last
+// keys do not wait for the stage of its first values, and packed words are on
+// their way while others are turned into halves.  Any other subtile is made on
+// its own between two runs, when no word is held.
 template <int FMT, bool SHARED>
-__device__ __forceinline__ void produce(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C, UnitSrc<FMT>& unit,
-                                        uint32_t k_tiles, uint32_t v_tiles, int sub) {
+__device__ __forceinline__ void produce(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C,
+                                        const UnitSrc<FMT>& unit, uint32_t k_tiles, uint32_t v_tiles, int pw) {
+  constexpr int kValueStages = value_stages(SHARED);
   const int lane = threadIdx.x & 31;
-  const int first = C.work.first, tiles = C.work.tiles, nq = C.work.sq.nq;
+  const int first = C.work.first, last = C.work.tiles * kSubs, nq = C.work.sq.nq;
   const bool direct = A.c.shape.rope_theta <= 0.f && !A.c.shape.sparse;   // codes straight to halves
+  // tokens from `clear` on, and tiles that end below the sinks, hide from no row
   const int p_last = C.work.sq.n + (min(C.work.r0 + (SHARED ? 2 : 1) * kRows, C.work.rows) - 1) / C.work.gq;
-  SubWords<FMT> w;
-  SubSrc d;
+  const int clear = A.window > 0 ? p_last - A.window + 1 : 0;
 
-  enum { kPacked, kOther, kBadPage };
-  struct Plan {
-    int base, mode;
-    bool two;
+  auto wait_keys = [&](int x) {
+    const int g = x / kSubs;
+    return warp_wait(&C.k_empty[g % kStages], ((g / kStages) & 1) ^ 1, &C.abort);
   };
-  auto plan = [&](int g) {
-    Plan p;
-    const int t0 = range.tile(first + g) * kKeys;
-    p.base = t0 + kTile * sub;
-    // rows may see part of a tile at the window's edges only
-    const bool edge = A.window > 0 && t0 <= p_last - A.window && t0 + kKeys > A.sinks;
-    p.mode = direct && nq - p.base >= kTile && !edge ? kPacked : kOther;
-    if (nq > p.base && !sub_src<FMT>(unit, p.base / kTile, d)) p.mode = kBadPage;
-    p.two = FMT == 2 || (FMT == 6 && d.two);
-    return p;
+  auto wait_values = [&](int x) {
+    const int g = x / kSubs;
+    return warp_wait(&C.v_empty[g % kValueStages], ((g / kValueStages) & 1) ^ 1, &C.abort);
+  };
+  auto hand_over = [&](uint64_t* bar) {
+    fence_async();
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar);
+  };
+  auto key_tile = [&](int x) { return k_tiles + (x / kSubs) % kStages * kTileBytes16; };
+  auto value_tile = [&](int x) { return v_tiles + (x / kSubs) % kValueStages * kTileBytes16; };
+  auto packed = [&](int x, SubSrc& d) {
+    const int t0 = range.tile(first + x / kSubs) * kKeys, base = t0 + kTile * (x % kSubs);
+    return direct && nq - base >= kTile && (t0 >= clear || t0 + kKeys <= A.sinks) &&
+           sub_src<FMT>(unit, base / kTile, d);
   };
 
-  if (tiles == 0) return;
-  Plan cur = plan(0);
-  if (cur.mode == kPacked) {
+  int x = pw;
+  while (x < last) {
+    SubSrc d;
+    if (!packed(x, d)) {
+      // The softmax reads the description when the scores are there, so it has
+      // to be complete before the keys are handed over: rows that need a look
+      // give their values first.
+      if (!wait_keys(x) || !wait_values(x)) return;
+      const int g = x / kSubs, sub = x % kSubs;
+      const int kind = produce_other<FMT>(A, C, range.tile(first + g) * kKeys + kTile * sub, key_tile(x), value_tile(x),
+                                          sub, C.info[g % kInfos]);
+      if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
+      hand_over(&C.k_full[g % kStages]);
+      hand_over(&C.v_full[g % kValueStages]);
+      x += kProducers;
+      continue;
+    }
+    SubWords<FMT> w;
     load_keys<FMT>(d, w);
-    load_values<FMT>(d, w);
-  }
-  for (int g = 0; g < tiles; ++g) {
-    const int st = g & 1;
-    const uint32_t parity = ((g >> 1) & 1) ^ 1;
-    const uint32_t kt = k_tiles + st * kTileBytes16, vt = v_tiles + st * kTileBytes16;
-    if (!warp_wait(&C.k_empty[st], parity, &C.abort)) return;
-    int kind = 0;
-    if (cur.mode == kPacked) {
-      if (FMT == 6 && cur.two) keys_to_tile<FMT, 2>(w, kt, sub);
-      else keys_to_tile<FMT, SubWords<FMT>::kBits>(w, kt, sub);
-    } else {
-      // The softmax reads the description when the scores are there, so it
-      // has to be complete before the keys are handed over: rows that need a
-      // look give their values now.
-      if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
-      kind = produce_other<FMT>(A, C, cur.base, min(max(nq - cur.base, 0), kTile), cur.mode != kBadPage, kt, vt, sub,
-                                C.info[g % kInfos]);
-      w = SubWords<FMT>{};                   // nothing to keep over the call
+    bool more, two = false;                  // two: the held values have 2-bit codes
+    for (int y = -1;; y = x, x += kProducers) {
+      // keys of x
+      const int g = x / kSubs;
+      if (!wait_keys(x)) return;
+      const bool two_here = d.two;
+      if (FMT == 6 && two_here) keys_to_tile<FMT, 2>(w, key_tile(x), x % kSubs);
+      else keys_to_tile<FMT, SubWords<FMT>::kBits>(w, key_tile(x), x % kSubs);
+      if (lane == 0) C.info[g % kInfos].kind[x % kSubs] = 0;
+      hand_over(&C.k_full[g % kStages]);
+      const SubSrc here = d;
+      more = x + kProducers < last && packed(x + kProducers, d);
+      if (more) load_keys<FMT>(d, w);
+      // values of y, the subtile before
+      if (y >= 0) {
+        if (!wait_values(y)) return;
+        if (FMT == 6 && two) values_to_tile<FMT, 2>(w, value_tile(y), y % kSubs);
+        else values_to_tile<FMT, SubWords<FMT>::kBits>(w, value_tile(y), y % kSubs);
+        hand_over(&C.v_full[(y / kSubs) % kValueStages]);
+      }
+      load_values<FMT>(here, w);
+      two = two_here;
+      if (!more) break;
     }
-    if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
-    fence_async();
-    __syncwarp();
-    if (lane == 0) bar_arrive(&C.k_full[st]);
-    Plan next = cur;
-    const bool more = g + 1 < tiles;
-    if (more) {
-      next = plan(g + 1);
-      if (next.mode == kPacked) load_keys<FMT>(d, w);
-    }
-    if (cur.mode == kPacked) {
-      if (!warp_wait(&C.v_empty[st], parity, &C.abort)) return;
-      if (FMT == 6 && cur.two) values_to_tile<FMT, 2>(w, vt, sub);
-      else values_to_tile<FMT, SubWords<FMT>::kBits>(w, vt, sub);
-    }
-    fence_async();
-    __syncwarp();
-    if (lane == 0) bar_arrive(&C.v_full[st]);
-    if (more && next.mode == kPacked) load_values<FMT>(d, w);
-    cur = next;
+    if (!wait_values(x)) return;
+    if (FMT == 6 && two) values_to_tile<FMT, 2>(w, value_tile(x), x % kSubs);
+    else values_to_tile<FMT, SubWords<FMT>::kBits>(w, value_tile(x), x % kSubs);
+    hand_over(&C.v_full[(x / kSubs) % kValueStages]);
+    x += kProducers;
   }
 }
 
-// The products of stream i, issued by the first warp of its softmax (the whole
-// warp waits, one elected thread issues; descriptors are warp-uniform):
-// scores of the stream's tile `it`, and its P V.  A stream's next scores
-// follow its P V, whose P they overwrite (the tensor core takes the products
-// of one thread in order); the streams alternate, so that one's softmax runs
-// while the other's products do.  False: a wait was given up.
-struct Products {
-  uint64_t q, k, v;            // operand descriptors: the stream's rows, stage 0 of the keys and of the values
-  uint32_t s, o;               // TMEM columns of the stream's scores (P in their second half) and output
-};
+// The products, issued by one elected thread of the last warp (the whole warp
+// waits; everything that addresses operands is warp-uniform).  Each stream's
+// scores come in two blocks of 64 keys, so that a block's softmax runs while
+// the other block's P V and next scores do; a block's next scores follow its
+// P V, whose P they overwrite (the tensor core takes one thread's products in
+// order).  False: a wait was given up.
 constexpr uint32_t kStageStep = kTileBytes16 >> 4;
 
 template <bool SHARED>
-__device__ __forceinline__ bool issue_scores(ChunkCtrl& C, const Products& P, int i, int it) {
-  const int g = SHARED ? it : 2 * it + i, st = g & 1;
-  if (!warp_wait(&C.k_full[st], (g >> 1) & 1, &C.abort)) return false;
-  tc_after();
-  const uint64_t k = P.k + st * kStageStep;
-  if (elect_one()) {
+__device__ __forceinline__ bool issue_all(ChunkCtrl& C, uint32_t q_tiles, uint32_t k_tiles, uint32_t v_tiles) {
+  constexpr int kValueStages = value_stages(SHARED);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, C.tmem, 0);
+  const int n0 = __shfl_sync(0xffffffffu, C.work.stream_tiles[0], 0), n1 = __shfl_sync(0xffffffffu, C.work.stream_tiles[1], 0);
+  const uint64_t q0 = operand_desc(q_tiles, 16), k0 = operand_desc(k_tiles, 16), v0 = operand_desc(v_tiles, kBlockBytes);
+  // scores of half h of stream i's tile `it`; `done`: the last that read the keys
+  auto scores = [&](int i, int it, int h, bool done) {
+    const int st = (SHARED ? it : i) & 1;
+    const uint64_t q = q0 + (SHARED ? i : 0) * kStageStep, k = k0 + st * kStageStep + ((h * kHalf * 128) >> 4);
+    const uint32_t d = tm_s(tmem, i) + kHalf * h;
+    if (elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const uint64_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;   // 16 channels on
-      mma_ss(P.s, P.q + off, k + off, kIdescQK, kk > 0);
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint64_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;   // 16 channels on
+        mma_ss(d, q + off, k + off, kIdescQK, kk > 0);
+      }
+      if (done) tc_commit(&C.k_empty[st]);
+      tc_commit(&C.s_full[i][h]);
     }
-    tc_commit(&C.k_empty[st]);
-    tc_commit(&C.s_full[i]);
-  }
-  __syncwarp();
-  return true;
-}
-template <bool SHARED>
-__device__ __forceinline__ bool issue_values(ChunkCtrl& C, const Products& P, int i, int it, bool last) {
-  const int g = SHARED ? it : 2 * it + i, st = g & 1;
-  if (!warp_wait(&C.p_ready[i], it & 1, &C.abort)) return false;
-  if (!warp_wait(&C.v_full[st], (g >> 1) & 1, &C.abort)) return false;
-  tc_after();
-  const uint64_t v = P.v + st * kStageStep;
-  const uint32_t add = it > 0;
-  if (elect_one()) {
+    __syncwarp();
+  };
+  auto values = [&](int i, int it, int h, bool done) {
+    const int st = (SHARED ? it : 2 * it + i) % kValueStages;
+    const uint64_t v = v0 + st * kStageStep + ((h * kHalf * 128) >> 4);
+    const uint32_t d = tm_o(tmem, i), p = tm_s(tmem, i) + kHalf * h, add = it > 0 || h > 0;
+    if (elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)                         // 16 tokens on: 16 rows of 128 bytes
-      mma_ts(P.o, P.s + kPColumn + 8 * kk, v + ((kk * 16 * 128) >> 4), kIdescPV, kk > 0 ? 1u : add);
-    tc_commit(&C.v_empty[st]);
-    if (last) tc_commit(&C.o_done[i]);
-  }
-  __syncwarp();
+      for (int kk = 0; kk < 4; ++kk)                       // 16 tokens on: 16 rows of 128 bytes
+        mma_ts(d, p + 8 * kk, v + ((kk * 16 * 128) >> 4), kIdescPV, kk > 0 ? 1u : add);
+      if (done) tc_commit(&C.v_empty[st]);
+      tc_commit(&C.o_done[i]);
+    }
+    __syncwarp();
+  };
+  // stage of a stream's tile: SHARED, tile it for both; else tile 2 it + i
+  auto full = [&](uint64_t* bar, int stages, int i, int it) {
+    const int g = SHARED ? it : 2 * it + i;
+    return warp_wait(bar + g % stages, (g / stages) & 1, &C.abort);
+  };
+  const int last = SHARED && n1 > 0 ? 1 : 0;               // SHARED: the stream that reads a tile last
+  for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < 2; ++i) {
+      if ((i ? n1 : n0) == 0) continue;
+      if (h == 0) {
+        if (!full(C.k_full, kStages, i, 0)) return false;
+        tc_after();
+      }
+      scores(i, 0, h, h == 1 && (!SHARED || i == last));
+    }
+  for (int it = 0; it < n0; ++it)
+    for (int y = 0; y < 4; ++y) {
+      const int h = SHARED ? y >> 1 : y & 1, i = SHARED ? y & 1 : y >> 1;
+      const int n = i ? n1 : n0;
+      if (it >= n) continue;
+      if (!warp_wait(&C.p_ready[i][h], it & 1, &C.abort)) return false;
+      if (h == 0 && !full(C.v_full, kValueStages, i, it)) return false;
+      tc_after();
+      const bool done = h == 1 && (!SHARED || i == last);
+      values(i, it, h, done);
+      if (it + 1 >= n) continue;
+      if (h == 0) {
+        if (!full(C.k_full, kStages, i, it + 1)) return false;
+        tc_after();
+      }
+      scores(i, it + 1, h, done);
+    }
   return true;
 }
-// After a wait that was given up: the products this thread has in flight end
-// before TMEM is freed (again with a limit).
-__device__ __forceinline__ void drain(ChunkCtrl& C, int i) {
-  tc_commit(&C.drained[i]);
+// After a wait that was given up: the products in flight end before TMEM is
+// freed (again with a limit).
+__device__ __forceinline__ void drain(ChunkCtrl& C) {
+  tc_commit(&C.drained);
   const unsigned long long t0 = now_ns();
-  while (!bar_try(&C.drained[i], 0) && now_ns() - t0 < kWaitNs) {}
+  while (!bar_try(&C.drained, 0) && now_ns() - t0 < kWaitNs) {}
 }
 
 struct RowState {
@@ -372,20 +422,25 @@ struct Scaling {
   float kmul, vlog, vinv;
 };
 
-// The softmax of one tile for one stream; the thread owns one row.
-template <bool SHARED>
-__device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo& info, const Scaling& packed, int t0, int p_row, int p_lo,
-                                          int p_hi, float cm, bool started, uint32_t ts, uint32_t to, RowState& r) {
-  const uint2 kinds = *reinterpret_cast<const uint2*>(info.kind);
-  // warp-uniform: every token of the tile is visible to every row, and the whole tile has one scaling
-  const bool plain = t0 + kKeys - 1 <= p_lo && (A.window <= 0 || t0 > p_hi - A.window || t0 + kKeys <= A.sinks) &&
-                     kinds.x == kinds.y && kinds.x == (kinds.x & 0xFFu) * 0x01010101u && (kinds.x & 0xFFu) != 2u;
+// The softmax of half a tile (64 tokens from t0 on, subtiles s0 ... s0 + 3) for
+// one stream; the thread owns one row.  `turn`: which half of the stream's this is.
+__device__ __forceinline__ void soft_half(const ChunkAttnArgs& A, ChunkCtrl& C, int i, int turn, const TileInfo& info,
+                                          const Scaling& packed, int t0, int s0, int p_row, int p_lo, int p_hi, float cm,
+                                          uint32_t ts, uint32_t to, RowState& r, bool& ok) {
+  const uint32_t kinds = *reinterpret_cast<const uint32_t*>(info.kind + s0);
+  // warp-uniform: every token is visible to every row, and all have one scaling
+  const bool plain = t0 + kHalf - 1 <= p_lo && (A.window <= 0 || t0 > p_hi - A.window || t0 + kHalf <= A.sinks) &&
+                     kinds == (kinds & 0xFFu) * 0x01010101u && (kinds & 0xFFu) != 2u;
   auto raise = [&](float top) {              // the row's reference, and O with it if it moves
     const bool up = top > r.m + kSlack || (r.m == -INFINITY && top > -INFINITY);
+    if (!__any_sync(0xffffffffu, up)) return;
     const float mn = up ? top : r.m;
     const float f = r.m == -INFINITY ? (up ? 0.f : 1.f) : (up ? ex2(r.m - mn) : 1.f);
-    if (started && __any_sync(0xffffffffu, up && r.m != -INFINITY)) {
-      // the scores are complete, so the products before them are: O is at rest
+    if (turn > 0 && __any_sync(0xffffffffu, up && r.m != -INFINITY)) {
+      // O is at rest once the P V of the half before this is done (the one
+      // before that is: these scores were issued behind it)
+      ok = warp_wait(&C.o_done[i], (turn - 1) & 1, &C.abort);
+      tc_after();
       const float fo = r.m == -INFINITY ? 1.f : f;             // O is zero then
 #pragma unroll 1
       for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
@@ -393,7 +448,7 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
         tc_ld16(o, to + c0);
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] *= fo;
+        for (int u = 0; u < 16; ++u) o[u] *= fo;
         tc_st16(to + c0, reinterpret_cast<uint32_t*>(o));
       }
       tc_wait_st();
@@ -402,47 +457,35 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
     r.m = mn;
   };
   if (plain) {
-    // two passes over the scores in TMEM: a row does not fit the registers
-    const bool own = (kinds.x & 0xFFu) == 0u;
+    const bool own = (kinds & 0xFFu) == 0u;
     const float k = own ? cm * packed.kmul : cm, vlog = own ? packed.vlog : 0.f;
+    float x[kHalf];
+    tc_ld32(x, ts);
+    tc_ld32(x + 32, ts + 32);
+    tc_wait_ld();
     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-    for (int c0 = 0; c0 < kKeys; c0 += 64) {
-      float x[64];
-      tc_ld32(x, ts + c0);
-      tc_ld32(x + 32, ts + c0 + 32);
-      tc_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 64; i += 8) {
+    for (int c = 0; c < kHalf; c += 8) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) t4[u] = fmaxf(fmaxf(t4[u], x[i + 2 * u]), x[i + 2 * u + 1]);
-      }
+      for (int u = 0; u < 4; ++u) t4[u] = fmaxf(fmaxf(t4[u], x[c + 2 * u]), x[c + 2 * u + 1]);
     }
     raise(fmaf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), k, vlog));
     const float off = vlog - (r.m == -INFINITY ? 0.f : r.m);
     const pair_t k2 = pair(k, k), off2 = pair(off, off);
     pair_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-    // from the upper half down: P lies over scores that have been read
-#pragma unroll 1
-    for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {
-      float x[64];
-      tc_ld32(x, ts + c0);
-      tc_ld32(x + 32, ts + c0 + 32);
-      tc_wait_ld();
 #pragma unroll
-      for (int c1 = 0; c1 < 64; c1 += 32) {
-        uint32_t p[16];
+    for (int c0 = 0; c0 < kHalf; c0 += 32) {
+      uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a, b;
-          unpair(pair_fma(pair(x[c1 + 2 * i], x[c1 + 2 * i + 1]), k2, off2), a, b);
-          a = ex2(a);
-          b = ex2(b);
-          sum[i & 1] = pair_add(sum[i & 1], pair(a, b));
-          p[i] = pack_h2(a, b);
-        }
-        tc_st16(ts + kPColumn + (c0 + c1) / 2, p);
+      for (int u = 0; u < 16; ++u) {
+        float a, b;
+        unpair(pair_fma(pair(x[c0 + 2 * u], x[c0 + 2 * u + 1]), k2, off2), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        sum[u & 1] = pair_add(sum[u & 1], pair(a, b));
+        p[u] = pack_h2(a, b);
       }
+      tc_st16(ts + c0 / 2, p);
     }
     float a, b;
     unpair(pair_add(sum[0], sum[1]), a, b);
@@ -454,23 +497,23 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
       return kind == 0 ? packed : kind == 1 ? Scaling{1.f, 0.f, 1.f} : Scaling{info.kmul[sub], info.vlog[sub], info.vinv[sub]};
     };
     auto bad_bits = [&](int sub) { return info.kind[sub] == 2 ? info.bad[sub] : 0u; };
-    auto scores = [&](int sub, float (&x)[16]) {
-      tc_ld16(x, ts + kTile * sub);
+    auto scores = [&](int j, float (&x)[16]) {
+      tc_ld16(x, ts + kTile * j);
       tc_wait_ld();
-      const Scaling sc = scaling(sub);
+      const Scaling sc = scaling(s0 + j);
       const float k = cm * sc.kmul, vlog = sc.vlog;
-      const bool none = bad_bits(sub) >> 16;
+      const bool none = bad_bits(s0 + j) >> 16;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const int t = t0 + kTile * sub + row_of_token(c);      // the order is its own inverse
+        const int t = t0 + kTile * j + row_of_token(c);        // the order is its own inverse
         x[c] = !none && key_visible(t, p_row, A.window, A.sinks) ? fmaf(x[c], k, vlog) : -INFINITY;
       }
     };
     float top = -INFINITY;
 #pragma unroll 1
-    for (int sub = 0; sub < kSubs; ++sub) {
+    for (int j = 0; j < kSubs / 2; ++j) {
       float x[16];
-      scores(sub, x);
+      scores(j, x);
 #pragma unroll
       for (int c = 0; c < 16; ++c) top = fmaxf(top, x[c]);
     }
@@ -478,10 +521,10 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
     const float ref = r.m == -INFINITY ? 0.f : r.m;
     float l = 0.f;
 #pragma unroll 1
-    for (int sub = kSubs - 1; sub >= 0; --sub) {             // downwards: see above
+    for (int j = 0; j < kSubs / 2; ++j) {                      // P lies over scores that have been read
       float x[16], sum = 0.f;
-      scores(sub, x);
-      const uint32_t bad = bad_bits(sub);
+      scores(j, x);
+      const uint32_t bad = bad_bits(s0 + j);
       uint32_t p[8];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
@@ -490,9 +533,9 @@ __device__ __forceinline__ void soft_tile(const ChunkAttnArgs& A, const TileInfo
         sum += x[c];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = pack_h2(x[2 * i], x[2 * i + 1]);
-      tc_st8(ts + kPColumn + 8 * sub, p);
-      l = fmaf(sum, scaling(sub).vinv, l);
+      for (int u = 0; u < 8; ++u) p[u] = pack_h2(x[2 * u], x[2 * u + 1]);
+      tc_st8(ts + 8 * j, p);
+      l = fmaf(sum, scaling(s0 + j).vinv, l);
     }
     r.l += l;
   }
@@ -542,27 +585,17 @@ __device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W,
 
 // The softmax of stream i; this thread has row `row` of the stream's rows.
 template <int FMT, bool SHARED>
-__device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C, uint32_t q_tiles,
-                                       uint32_t k_tiles, uint32_t v_tiles, int i, int row, uint8_t* generic) {
+__device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C, int i, int row,
+                                       uint8_t* generic) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Work& W = C.work;
-  const int tiles = W.stream_tiles[i], other_tiles = W.stream_tiles[1 - i];
+  const int tiles = W.stream_tiles[i];
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
   const uint32_t ts = tm_s(C.tmem, i) + lanes, to = tm_o(C.tmem, i) + lanes;
   const int R = W.r0 + (SHARED ? i * kRows : 0) + row;
   const bool idle = R - lane >= W.rows;                      // no row of this warp is real
   RowState r{-INFINITY, 0.f};
-  const bool issuer = (warp & 3) == 0;                       // this warp issues the stream's products
   bool ok = true;
-  Products P;
-  {
-    const uint32_t tmem = __shfl_sync(0xffffffffu, C.tmem, 0);
-    P.q = operand_desc(q_tiles + (SHARED ? i : 0) * kTileBytes16, 16);
-    P.k = operand_desc(k_tiles, 16);
-    P.v = operand_desc(v_tiles, kBlockBytes);
-    P.s = tm_s(tmem, i);
-    P.o = tm_o(tmem, i);
-  }
   {
     const int last = W.rows - 1, n = W.sq.n, w0 = R - lane;
     const int p_row = n + min(R, last) / W.gq;
@@ -574,35 +607,23 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& 
       packed = Scaling{A.c.fp8_scale[W.kv], log2f(vs), 1.f / vs};
     }
     const int first = W.first;
-    if (issuer && tiles > 0) ok = issue_scores<SHARED>(C, P, i, 0);
-    for (int it = 0; it < tiles && ok; ++it) {
-      const int g = SHARED ? it : 2 * it + i;
-      if (!(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
+    for (int x = 0; x < 2 * tiles && ok; ++x) {
+      const int it = x >> 1, h = x & 1, g = SHARED ? it : 2 * it + i;
+      if (!(ok = warp_wait(&C.s_full[i][h], it & 1, &C.abort))) break;
       if (!idle) {
         tc_after();
-        soft_tile<SHARED>(A, C.info[g % kInfos], packed, range.tile(first + g) * kKeys, p_row, p_lo, p_hi, cm, it > 0, ts,
-                          to, r);
+        soft_half(A, C, i, x, C.info[g % kInfos], packed, range.tile(first + g) * kKeys + kHalf * h, kSubs / 2 * h, p_row,
+                  p_lo, p_hi, cm, ts + kHalf * h, to, r, ok);
         tc_wait_st();
         tc_before();
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(&C.p_ready[i]);
-      if (issuer) {
-        // The streams take turns at the tensor cores, a stream's P V and next
-        // scores together: left to themselves both would compute and both
-        // would multiply at the same time.
-        if (i == 0) ok = it == 0 || it > other_tiles || warp_wait(&C.turn[0], (it - 1) & 1, &C.abort);
-        else ok = warp_wait(&C.turn[1], it & 1, &C.abort);
-        ok = ok && issue_values<SHARED>(C, P, i, it, it + 1 == tiles);
-        if (ok && it + 1 < tiles) ok = issue_scores<SHARED>(C, P, i, it + 1);
-        if (lane == 0) bar_arrive(&C.turn[1 - i]);
-      }
+      if (lane == 0) bar_arrive(&C.p_ready[i][h]);
     }
   }
   const bool any = tiles > 0;
-  if (ok && any) ok = warp_wait(&C.o_done[i], 0, &C.abort);
-  if (!ok && issuer && elect_one()) drain(C, i);
-  __syncwarp();
+  // the last two P V may both be under way: a parity tells one phase from the next only
+  if (ok && any) ok = warp_wait(&C.o_done[i], 0, &C.abort) && warp_wait(&C.o_done[i], 1, &C.abort);
   tc_after();
   const float one[2] = {1.f, 0.f};
   if (SHARED) {
@@ -630,7 +651,7 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& 
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     if (i == 0 && ok && !idle) {
       const float m1 = C.ml[row][0], l1 = C.ml[row][1];
-      const bool two = other_tiles > 0;
+      const bool two = W.stream_tiles[1] > 0;
       const float M = fmaxf(r.m, m1), ref = M == -INFINITY ? 0.f : M;
       const float f[2] = {ex2(r.m - ref), two && m1 != -INFINITY ? ex2(m1 - ref) : 0.f};
       const RowState j{M, r.l * f[0] + (two ? l1 * f[1] : 0.f)};
@@ -676,18 +697,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
   const uint32_t q_tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t k_tiles = q_tiles + (SHARED ? 2 : 1) * kTileBytes16, v_tiles = k_tiles + kStages * kTileBytes16;
   uint8_t* generic = smem_raw + (q_tiles - smem_u32(smem_raw));
-  ChunkCtrl& C = *reinterpret_cast<ChunkCtrl*>(generic + (v_tiles + kStages * kTileBytes16 - q_tiles));
+  ChunkCtrl& C = *reinterpret_cast<ChunkCtrl*>(generic + (v_tiles + value_stages(SHARED) * kTileBytes16 - q_tiles));
   if (tid == 0) {
-    const int users = SHARED && W.stream_tiles[1] > 0 ? 2 : 1;     // streams that read each tile
     for (int i = 0; i < kStages; ++i) {
-      bar_init(&C.k_full[i], kSubs); bar_init(&C.k_empty[i], users);
-      bar_init(&C.v_full[i], kSubs); bar_init(&C.v_empty[i], users);
+      bar_init(&C.k_full[i], kSubs); bar_init(&C.k_empty[i], 1);
     }
+    for (int i = 0; i < kMaxValueStages; ++i) { bar_init(&C.v_full[i], kSubs); bar_init(&C.v_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&C.s_full[i], 1); bar_init(&C.p_ready[i], 4);
-      bar_init(&C.o_done[i], 1); bar_init(&C.turn[i], 1); bar_init(&C.drained[i], 1);
+      for (int h = 0; h < 2; ++h) { bar_init(&C.s_full[i][h], 1); bar_init(&C.p_ready[i][h], 4); }
+      bar_init(&C.o_done[i], 1);
     }
-      C.abort = 0;
+    bar_init(&C.drained, 1);
+    C.abort = 0;
     C.work = W;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -732,11 +753,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
   tc_after();
   const uint32_t tmem = C.tmem;
 
-  if (warp >= kProducerWarp) {
+  if (warp == kMmaWarp) {
+    if (!issue_all<SHARED>(C, q_tiles, k_tiles, v_tiles) && elect_one()) drain(C);
+    __syncwarp();
+  } else if (warp >= kProducerWarp) {
     produce<FMT, SHARED>(A, range, C, unit, k_tiles, v_tiles, warp - kProducerWarp);
   } else {
     const int i = __shfl_sync(0xffffffffu, warp >> 2, 0), row = tid % kRows;   // warp-uniform for the compiler too
-    soften<FMT, SHARED>(A, range, C, q_tiles, k_tiles, v_tiles, i, row, generic);
+    soften<FMT, SHARED>(A, range, C, i, row, generic);
   }
   __syncthreads();
   if (warp == kProducerWarp) {

@@ -186,7 +186,7 @@ template <int FMT> struct SubWords {
   static constexpr int kBits = FMT == 6 ? 4 : (FMT == 16 ? 8 : FMT);
   static constexpr int kKW = kBits == 8 ? 16 : 8;            // key words: 8 rows of one or two
   static constexpr int kVW = 2 * kBits;
-  static constexpr int kKM = FMT == 8 ? 0 : 8;
+  static constexpr int kKM = FMT == 8 ? 0 : (FMT == 2 || FMT == 6) ? 16 : 8;
   uint32_t k[kKW], v[kVW];
   uint32_t km[kKM ? kKM : 1];                                // key scales, then zeros, of the lane's channels (INT8: per row)
   uint32_t vm[FMT == 8 ? 1 : 4];                             // value (scale, zero) of the lane's four tokens
@@ -217,11 +217,12 @@ __device__ __forceinline__ void load_keys(const SubSrc& d, SubWords<FMT>& w) {
     for (int i = 0; i < 2; ++i) {
       const __half* m = d.km + i * kHeadDim;
       if (two) {
+        // word r of 8 holds channels (r, r + 8) of 16
         const uint4 a = *reinterpret_cast<const uint4*>(m + 16 * (j >> 1));
         const uint4 b = *reinterpret_cast<const uint4*>(m + 16 * (j >> 1) + 8);
-        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;    // word r of 8 holds channels (r, r + 8)
-        w.km[4 * i] = prmt(a.x, b.x, sel); w.km[4 * i + 1] = prmt(a.y, b.y, sel);
-        w.km[4 * i + 2] = prmt(a.z, b.z, sel); w.km[4 * i + 3] = prmt(a.w, b.w, sel);
+        uint32_t* k = w.km + 8 * i;
+        k[0] = a.x; k[1] = a.y; k[2] = a.z; k[3] = a.w;
+        k[4] = b.x; k[5] = b.y; k[6] = b.z; k[7] = b.w;
       } else {
         const uint4 a = *reinterpret_cast<const uint4*>(m + 8 * j);   // pairs (0,2) (1,3) (4,6) (5,7)
         w.km[4 * i] = a.x; w.km[4 * i + 1] = a.y; w.km[4 * i + 2] = a.z; w.km[4 * i + 3] = a.w;
@@ -257,8 +258,9 @@ __device__ __forceinline__ void keys_to_tile(const SubWords<FMT>& w, uint32_t ti
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if constexpr (BITS == 2) {
-        sc[k] = w.km[k];
-        zc[k] = w.km[4 + k];
+        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+        sc[k] = prmt(w.km[k], w.km[4 + k], sel);
+        zc[k] = prmt(w.km[8 + k], w.km[12 + k], sel);
       } else {
         sc[k] = prmt(w.km[k & 1], w.km[2 + (k & 1)], k < 2 ? 0x5410u : 0x7632u);
         zc[k] = prmt(w.km[4 + (k & 1)], w.km[6 + (k & 1)], k < 2 ? 0x5410u : 0x7632u);
