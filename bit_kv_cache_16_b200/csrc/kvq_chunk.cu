@@ -18,7 +18,7 @@ constexpr int kProducerWarp = 8;             // warps 0-3 and 4-7: softmax of st
 constexpr int kProducers = 7;
 constexpr int kMmaWarp = kProducerWarp + kProducers;            // issues every product
 constexpr int kChunkThreads = 32 * (kMmaWarp + 1);              // four warps per scheduler: 128 registers each
-constexpr int kHalf = kKeys / 2;             // keys per score block: each stream has two
+constexpr int kHalf = kKeys / 2;             // a row's softmax takes 64 keys at a time
 constexpr int kStages = 2;                   // key tiles in flight
 // Value tiles in flight.  A producer may have two subtiles of one tile, and
 // writes the values of the first before the keys of the second.  Paired
@@ -41,7 +41,7 @@ struct Work {
 
 struct ChunkCtrl {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kMaxValueStages], v_empty[kMaxValueStages];
-  uint64_t s_full[2][2], p_ready[2][2], o_done[2], drained;   // [stream][half of the tile]
+  uint64_t s_full[2], p_ready[2][2], o_done[2], finished[2], drained;   // [stream][half of the tile]
   uint32_t tmem;
   int abort;
   TileInfo info[kInfos];
@@ -149,9 +149,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-// fp16 x fp16 -> fp32, M = 128; N = 64 keys, or 128 channels (stored with channels contiguous).
-constexpr uint32_t kIdescQK = (1u << 4) | ((kHalf / 8) << 17) | (8u << 24);
-constexpr uint32_t kIdescPV = (1u << 4) | (16u << 17) | (8u << 24) | (1u << 16);
+// fp16 x fp16 -> fp32, M = N = 128; the value operand is stored with channels (N) contiguous.
+constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
@@ -308,11 +308,13 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, const TileRange&
 }
 
 // The products, issued by one elected thread of the last warp (the whole warp
-// waits; everything that addresses operands is warp-uniform).  Each stream's
-// scores come in two blocks of 64 keys, so that a block's softmax runs while
-// the other block's P V and next scores do; a block's next scores follow its
-// P V, whose P they overwrite (the tensor core takes one thread's products in
-// order).  False: a wait was given up.
+// waits; everything that addresses operands is warp-uniform).  P V of a tile's
+// first half runs while the softmax does the second; the next scores follow
+// the second P V, whose P they overwrite (the tensor core takes one thread's
+// products in order), while the other stream's softmax runs.  (Scores in two
+// blocks of 64 keys, each with its own next product, were slower: a product
+// of N = 64 takes 58 cycles, one of N = 128 about 64, both bound by the query
+// operand's way from shared memory.)  False: a wait was given up.
 constexpr uint32_t kStageStep = kTileBytes16 >> 4;
 
 template <bool SHARED>
@@ -321,11 +323,11 @@ __device__ __forceinline__ bool issue_all(ChunkCtrl& C, uint32_t q_tiles, uint32
   const uint32_t tmem = __shfl_sync(0xffffffffu, C.tmem, 0);
   const int n0 = __shfl_sync(0xffffffffu, C.work.stream_tiles[0], 0), n1 = __shfl_sync(0xffffffffu, C.work.stream_tiles[1], 0);
   const uint64_t q0 = operand_desc(q_tiles, 16), k0 = operand_desc(k_tiles, 16), v0 = operand_desc(v_tiles, kBlockBytes);
-  // scores of half h of stream i's tile `it`; `done`: the last that read the keys
-  auto scores = [&](int i, int it, int h, bool done) {
+  // scores of stream i's tile `it`; `done`: the last that read the keys
+  auto scores = [&](int i, int it, bool done) {
     const int st = (SHARED ? it : i) & 1;
-    const uint64_t q = q0 + (SHARED ? i : 0) * kStageStep, k = k0 + st * kStageStep + ((h * kHalf * 128) >> 4);
-    const uint32_t d = tm_s(tmem, i) + kHalf * h;
+    const uint64_t q = q0 + (SHARED ? i : 0) * kStageStep, k = k0 + st * kStageStep;
+    const uint32_t d = tm_s(tmem, i);
     if (elect_one()) {
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
@@ -333,11 +335,11 @@ __device__ __forceinline__ bool issue_all(ChunkCtrl& C, uint32_t q_tiles, uint32
         mma_ss(d, q + off, k + off, kIdescQK, kk > 0);
       }
       if (done) tc_commit(&C.k_empty[st]);
-      tc_commit(&C.s_full[i][h]);
+      tc_commit(&C.s_full[i]);
     }
     __syncwarp();
   };
-  auto values = [&](int i, int it, int h, bool done) {
+  auto values = [&](int i, int it, int h, bool done, bool last) {
     const int st = (SHARED ? it : 2 * it + i) % kValueStages;
     const uint64_t v = v0 + st * kStageStep + ((h * kHalf * 128) >> 4);
     const uint32_t d = tm_o(tmem, i), p = tm_s(tmem, i) + kHalf * h, add = it > 0 || h > 0;
@@ -347,6 +349,7 @@ __device__ __forceinline__ bool issue_all(ChunkCtrl& C, uint32_t q_tiles, uint32
         mma_ts(d, p + 8 * kk, v + ((kk * 16 * 128) >> 4), kIdescPV, kk > 0 ? 1u : add);
       if (done) tc_commit(&C.v_empty[st]);
       tc_commit(&C.o_done[i]);
+      if (last) tc_commit(&C.finished[i]);
     }
     __syncwarp();
   };
@@ -355,32 +358,28 @@ __device__ __forceinline__ bool issue_all(ChunkCtrl& C, uint32_t q_tiles, uint32
     const int g = SHARED ? it : 2 * it + i;
     return warp_wait(bar + g % stages, (g / stages) & 1, &C.abort);
   };
-  const int last = SHARED && n1 > 0 ? 1 : 0;               // SHARED: the stream that reads a tile last
-  for (int h = 0; h < 2; ++h)
-    for (int i = 0; i < 2; ++i) {
-      if ((i ? n1 : n0) == 0) continue;
-      if (h == 0) {
-        if (!full(C.k_full, kStages, i, 0)) return false;
-        tc_after();
-      }
-      scores(i, 0, h, h == 1 && (!SHARED || i == last));
-    }
+  const int closer = SHARED && n1 > 0 ? 1 : 0;             // SHARED: the stream that reads a tile last
+  for (int i = 0; i < 2; ++i) {
+    if ((i ? n1 : n0) == 0) continue;
+    if (!full(C.k_full, kStages, i, 0)) return false;
+    tc_after();
+    scores(i, 0, !SHARED || i == closer);
+  }
   for (int it = 0; it < n0; ++it)
-    for (int y = 0; y < 4; ++y) {
-      const int h = SHARED ? y >> 1 : y & 1, i = SHARED ? y & 1 : y >> 1;
+    for (int i = 0; i < 2; ++i) {
       const int n = i ? n1 : n0;
       if (it >= n) continue;
-      if (!warp_wait(&C.p_ready[i][h], it & 1, &C.abort)) return false;
-      if (h == 0 && !full(C.v_full, kValueStages, i, it)) return false;
+      const bool done = !SHARED || i == closer;
+      if (!full(C.v_full, kValueStages, i, it) || !warp_wait(&C.p_ready[i][0], it & 1, &C.abort)) return false;
       tc_after();
-      const bool done = h == 1 && (!SHARED || i == last);
-      values(i, it, h, done);
+      values(i, it, 0, false, false);
+      if (!warp_wait(&C.p_ready[i][1], it & 1, &C.abort)) return false;
+      tc_after();
+      values(i, it, 1, done, it + 1 == n);
       if (it + 1 >= n) continue;
-      if (h == 0) {
-        if (!full(C.k_full, kStages, i, it + 1)) return false;
-        tc_after();
-      }
-      scores(i, it + 1, h, done);
+      if (!full(C.k_full, kStages, i, it + 1)) return false;
+      tc_after();
+      scores(i, it + 1, done);
     }
   return true;
 }
@@ -609,7 +608,7 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& 
     const int first = W.first;
     for (int x = 0; x < 2 * tiles && ok; ++x) {
       const int it = x >> 1, h = x & 1, g = SHARED ? it : 2 * it + i;
-      if (!(ok = warp_wait(&C.s_full[i][h], it & 1, &C.abort))) break;
+      if (h == 0 && !(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
       if (!idle) {
         tc_after();
         soft_half(A, C, i, x, C.info[g % kInfos], packed, range.tile(first + g) * kKeys + kHalf * h, kSubs / 2 * h, p_row,
@@ -622,8 +621,7 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& 
     }
   }
   const bool any = tiles > 0;
-  // the last two P V may both be under way: a parity tells one phase from the next only
-  if (ok && any) ok = warp_wait(&C.o_done[i], 0, &C.abort) && warp_wait(&C.o_done[i], 1, &C.abort);
+  if (ok && any) ok = warp_wait(&C.finished[i], 0, &C.abort);
   tc_after();
   const float one[2] = {1.f, 0.f};
   if (SHARED) {
@@ -704,8 +702,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     }
     for (int i = 0; i < kMaxValueStages; ++i) { bar_init(&C.v_full[i], kSubs); bar_init(&C.v_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
-      for (int h = 0; h < 2; ++h) { bar_init(&C.s_full[i][h], 1); bar_init(&C.p_ready[i][h], 4); }
-      bar_init(&C.o_done[i], 1);
+      bar_init(&C.s_full[i], 1); bar_init(&C.o_done[i], 1); bar_init(&C.finished[i], 1);
+      bar_init(&C.p_ready[i][0], 4); bar_init(&C.p_ready[i][1], 4);
     }
     bar_init(&C.drained, 1);
     C.abort = 0;
