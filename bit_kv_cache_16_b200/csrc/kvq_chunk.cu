@@ -36,6 +36,7 @@ struct Work {
   ChunkSeq sq;
   int b, kv, gq, r0, rows, split;
   int first, tiles;                          // tiles [first, first + tiles) of the range
+  TileRange range;
   int stream_tiles[2];
 };
 
@@ -49,6 +50,8 @@ struct ChunkCtrl {
   float ml[kRows][2];                        // paired streams: (m, l) of stream 1
   double freq[kHeadDim / 2];                 // RoPE pair frequencies
   Work work;                                 // kept here, not in every thread's registers
+  int clear;                                 // tokens from here on are hidden from no row of the CTA by the window
+  int2 seen[8];                              // the same for a softmax warp's rows, and its first row's position
 };
 
 __host__ __device__ constexpr int chunk_smem_bytes(bool shared_keys) {
@@ -225,15 +228,11 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
 // their way while others are turned into halves.  Any other subtile is made on
 // its own between two runs, when no word is held.
 template <int FMT, bool SHARED>
-__device__ __forceinline__ void produce(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C,
-                                        const UnitSrc<FMT>& unit, uint32_t k_tiles, uint32_t v_tiles, int pw) {
+__device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, const UnitSrc<FMT>& unit, uint32_t k_tiles, uint32_t v_tiles, int pw) {
   constexpr int kValueStages = value_stages(SHARED);
   const int lane = threadIdx.x & 31;
-  const int first = C.work.first, last = C.work.tiles * kSubs, nq = C.work.sq.nq;
-  const bool direct = A.c.shape.rope_theta <= 0.f && !A.c.shape.sparse;   // codes straight to halves
-  // tokens from `clear` on, and tiles that end below the sinks, hide from no row
-  const int p_last = C.work.sq.n + (min(C.work.r0 + (SHARED ? 2 : 1) * kRows, C.work.rows) - 1) / C.work.gq;
-  const int clear = A.window > 0 ? p_last - A.window + 1 : 0;
+  const volatile Work& W = C.work;           // read where it is used: registers are short
+  const int last = C.work.tiles * kSubs;
 
   auto wait_keys = [&](int x) {
     const int g = x / kSubs;
@@ -248,12 +247,17 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, const TileRange&
     __syncwarp();
     if (lane == 0) bar_arrive(bar);
   };
+  auto tile = [&](int x) {
+    const int y = W.first + x / kSubs, lead = W.range.lead;
+    return y < lead ? y : W.range.skip + y - lead;
+  };
   auto key_tile = [&](int x) { return k_tiles + (x / kSubs) % kStages * kTileBytes16; };
   auto value_tile = [&](int x) { return v_tiles + (x / kSubs) % kValueStages * kTileBytes16; };
   auto packed = [&](int x, SubSrc& d) {
-    const int t0 = range.tile(first + x / kSubs) * kKeys, base = t0 + kTile * (x % kSubs);
-    return direct && nq - base >= kTile && (t0 >= clear || t0 + kKeys <= A.sinks) &&
-           sub_src<FMT>(unit, base / kTile, d);
+    const int t0 = tile(x) * kKeys, base = t0 + kTile * (x % kSubs);
+    // codes go straight to halves; tokens past `clear` and tiles of sinks hide from no row
+    return A.c.shape.rope_theta <= 0.f && !A.c.shape.sparse && W.sq.nq - base >= kTile &&
+           (t0 >= *(volatile int*)&C.clear || t0 + kKeys <= A.sinks) && sub_src<FMT>(unit, base / kTile, d);
   };
 
   int x = pw;
@@ -265,7 +269,7 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, const TileRange&
       // give their values first.
       if (!wait_keys(x) || !wait_values(x)) return;
       const int g = x / kSubs, sub = x % kSubs;
-      const int kind = produce_other<FMT>(A, C, range.tile(first + g) * kKeys + kTile * sub, key_tile(x), value_tile(x),
+      const int kind = produce_other<FMT>(A, C, tile(x) * kKeys + kTile * sub, key_tile(x), value_tile(x),
                                           sub, C.info[g % kInfos]);
       if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
       hand_over(&C.k_full[g % kStages]);
@@ -421,108 +425,146 @@ struct Scaling {
   float kmul, vlog, vinv;
 };
 
-// The softmax of half a tile (64 tokens from t0 on, subtiles s0 ... s0 + 3) for
-// one stream; the thread owns one row.  `turn`: which half of the stream's this is.
-__device__ __forceinline__ void soft_half(const ChunkAttnArgs& A, ChunkCtrl& C, int i, int turn, const TileInfo& info,
-                                          const Scaling& packed, int t0, int s0, int p_row, int p_lo, int p_hi, float cm,
-                                          uint32_t ts, uint32_t to, RowState& r, bool& ok) {
-  const uint32_t kinds = *reinterpret_cast<const uint32_t*>(info.kind + s0);
-  // warp-uniform: every token is visible to every row, and all have one scaling
-  const bool plain = t0 + kHalf - 1 <= p_lo && (A.window <= 0 || t0 > p_hi - A.window || t0 + kHalf <= A.sinks) &&
-                     kinds == (kinds & 0xFFu) * 0x01010101u && (kinds & 0xFFu) != 2u;
-  auto raise = [&](float top) {              // the row's reference, and O with it if it moves
-    const bool up = top > r.m + kSlack || (r.m == -INFINITY && top > -INFINITY);
-    if (!__any_sync(0xffffffffu, up)) return;
-    const float mn = up ? top : r.m;
-    const float f = r.m == -INFINITY ? (up ? 0.f : 1.f) : (up ? ex2(r.m - mn) : 1.f);
-    if (turn > 0 && __any_sync(0xffffffffu, up && r.m != -INFINITY)) {
-      // O is at rest once the P V of the half before this is done (the one
-      // before that is: these scores were issued behind it)
-      ok = warp_wait(&C.o_done[i], (turn - 1) & 1, &C.abort);
-      tc_after();
-      const float fo = r.m == -INFINITY ? 1.f : f;             // O is zero then
+// One stream's softmax state in a thread: it owns one row.
+struct Row {
+  RowState r;
+  float cm;                                  // the row's factor: |softmax_scale| log2(e) 2^e
+  uint32_t ts, to;                           // TMEM addresses of the warp's scores and output
+};
+
+// Raises the row's reference to cover `top`, and O with it if it has to move;
+// `turn` is the number of the half tile in the stream.  False: a wait was
+// given up.
+__device__ __forceinline__ bool raise(ChunkCtrl& C, int i, int turn, float top, Row& w) {
+  RowState& r = w.r;
+  const bool up = top > r.m + kSlack || (r.m == -INFINITY && top > -INFINITY);
+  if (!__any_sync(0xffffffffu, up)) return true;
+  const float mn = up ? top : r.m;
+  const float f = r.m == -INFINITY ? (up ? 0.f : 1.f) : (up ? ex2(r.m - mn) : 1.f);
+  if (turn > 0 && __any_sync(0xffffffffu, up && r.m != -INFINITY)) {
+    // O is at rest once the P V of the half before this is done (the one
+    // before that is: a parity tells one phase from the next only)
+    if (!warp_wait(&C.o_done[i], (turn - 1) & 1, &C.abort)) return false;
+    tc_after();
+    const float fo = r.m == -INFINITY ? 1.f : f;               // O is zero then
 #pragma unroll 1
-      for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
-        float o[16];
-        tc_ld16(o, to + c0);
-        tc_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 16; ++u) o[u] *= fo;
-        tc_st16(to + c0, reinterpret_cast<uint32_t*>(o));
-      }
-      tc_wait_st();
-    }
-    r.l *= f;
-    r.m = mn;
-  };
-  if (plain) {
-    const bool own = (kinds & 0xFFu) == 0u;
-    const float k = own ? cm * packed.kmul : cm, vlog = own ? packed.vlog : 0.f;
-    float x[kHalf];
-    tc_ld32(x, ts);
-    tc_ld32(x + 32, ts + 32);
-    tc_wait_ld();
-    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int c = 0; c < kHalf; c += 8) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) t4[u] = fmaxf(fmaxf(t4[u], x[c + 2 * u]), x[c + 2 * u + 1]);
-    }
-    raise(fmaf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), k, vlog));
-    const float off = vlog - (r.m == -INFINITY ? 0.f : r.m);
-    const pair_t k2 = pair(k, k), off2 = pair(off, off);
-    pair_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-    for (int c0 = 0; c0 < kHalf; c0 += 32) {
-      uint32_t p[16];
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        float a, b;
-        unpair(pair_fma(pair(x[c0 + 2 * u], x[c0 + 2 * u + 1]), k2, off2), a, b);
-        a = ex2(a);
-        b = ex2(b);
-        sum[u & 1] = pair_add(sum[u & 1], pair(a, b));
-        p[u] = pack_h2(a, b);
-      }
-      tc_st16(ts + c0 / 2, p);
-    }
-    float a, b;
-    unpair(pair_add(sum[0], sum[1]), a, b);
-    r.l = fmaf(a + b, own ? packed.vinv : 1.f, r.l);
-  } else {
-    // subtile by subtile: its own scaling, hidden and missing tokens left out
-    auto scaling = [&](int sub) {
-      const int kind = info.kind[sub];
-      return kind == 0 ? packed : kind == 1 ? Scaling{1.f, 0.f, 1.f} : Scaling{info.kmul[sub], info.vlog[sub], info.vinv[sub]};
-    };
-    auto bad_bits = [&](int sub) { return info.kind[sub] == 2 ? info.bad[sub] : 0u; };
-    auto scores = [&](int j, float (&x)[16]) {
-      tc_ld16(x, ts + kTile * j);
+    for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
+      float o[16];
+      tc_ld16(o, w.to + c0);
       tc_wait_ld();
-      const Scaling sc = scaling(s0 + j);
-      const float k = cm * sc.kmul, vlog = sc.vlog;
-      const bool none = bad_bits(s0 + j) >> 16;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const int t = t0 + kTile * j + row_of_token(c);        // the order is its own inverse
-        x[c] = !none && key_visible(t, p_row, A.window, A.sinks) ? fmaf(x[c], k, vlog) : -INFINITY;
-      }
-    };
+      for (int u = 0; u < 16; ++u) o[u] *= fo;
+      tc_st16(w.to + c0, reinterpret_cast<uint32_t*>(o));
+    }
+    tc_wait_st();
+  }
+  r.l *= f;
+  r.m = mn;
+  return true;
+}
+
+__device__ __forceinline__ float most(float top, const float (&x)[32]) {
+  float t4[4] = {top, x[0], x[1], x[2]};
+#pragma unroll
+  for (int c = 3; c + 1 < 32; c += 2) t4[(c >> 1) & 3] = fmaxf(fmaxf(t4[(c >> 1) & 3], x[c]), x[c + 1]);
+  return fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), x[31]);
+}
+
+// 32 scores -> P (fp16, TMEM column `at` on); adds their weights to `sum`.
+__device__ __forceinline__ void weigh(const float (&x)[32], pair_t k2, pair_t off2, uint32_t at, pair_t (&sum)[2]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t p[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      float a, b;
+      unpair(pair_fma(pair(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]), k2, off2), a, b);
+      a = ex2(a);
+      b = ex2(b);
+      sum[u & 1] = pair_add(sum[u & 1], pair(a, b));
+      p[u] = pack_h2(a, b);
+    }
+    tc_st8(at + 8 * c, p);
+  }
+}
+__device__ __forceinline__ float total(const pair_t (&sum)[2]) {
+  float a, b;
+  unpair(pair_add(sum[0], sum[1]), a, b);
+  return a + b;
+}
+
+__device__ __forceinline__ void hand_over_p(ChunkCtrl& C, int i, int h) {
+  tc_wait_st();
+  tc_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(&C.p_ready[i][h]);
+}
+
+// A tile whose tokens are all visible to every row of the warp and have one
+// scaling.  Two halves of 64 keys: a row's scores of a half are held in
+// registers, and the second half's are on their way while the first is weighed.
+__device__ __forceinline__ bool soft_plain(ChunkCtrl& C, int i, int it, const Scaling& sc, Row& w) {
+  const float k = w.cm * sc.kmul;
+  const pair_t k2 = pair(k, k);
+  float xa[32], xb[32];
+  tc_ld32(xa, w.ts);
+  tc_ld32(xb, w.ts + 32);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    tc_wait_ld();
+    if (!raise(C, i, 2 * it + h, fmaf(most(most(-INFINITY, xa), xb), k, sc.vlog), w)) return false;
+    const float off = sc.vlog - (w.r.m == -INFINITY ? 0.f : w.r.m);
+    const pair_t off2 = pair(off, off);
+    pair_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    weigh(xa, k2, off2, w.ts + kHalf * h, sum);
+    if (h == 0) tc_ld32(xa, w.ts + kHalf);
+    weigh(xb, k2, off2, w.ts + kHalf * h + 16, sum);
+    if (h == 0) tc_ld32(xb, w.ts + kHalf + 32);
+    w.r.l = fmaf(total(sum), sc.vinv, w.r.l);
+    hand_over_p(C, i, h);
+  }
+  return true;
+}
+
+// Any other tile: subtile by subtile with its own scaling, hidden and missing
+// tokens left out.
+__device__ __forceinline__ bool soft_any(const ChunkAttnArgs& A, ChunkCtrl& C, int i, int it, int slot, const Scaling& packed,
+                                      int t0, int p_row, Row& w) {
+  const TileInfo& info = C.info[slot];
+  auto scaling = [&](int sub) {
+    const int kind = info.kind[sub];
+    return kind == 0 ? packed : kind == 1 ? Scaling{1.f, 0.f, 1.f} : Scaling{info.kmul[sub], info.vlog[sub], info.vinv[sub]};
+  };
+  auto bad_bits = [&](int sub) { return info.kind[sub] == 2 ? info.bad[sub] : 0u; };
+  auto scores = [&](int sub, float (&x)[16]) {
+    tc_ld16(x, w.ts + kTile * sub);
+    tc_wait_ld();
+    const Scaling sc = scaling(sub);
+    const float k = w.cm * sc.kmul, vlog = sc.vlog;
+    const bool none = bad_bits(sub) >> 16;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const int t = t0 + kTile * sub + row_of_token(c);        // the order is its own inverse
+      x[c] = !none && key_visible(t, p_row, A.window, A.sinks) ? fmaf(x[c], k, vlog) : -INFINITY;
+    }
+  };
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const int s0 = kSubs / 2 * h;
     float top = -INFINITY;
 #pragma unroll 1
     for (int j = 0; j < kSubs / 2; ++j) {
       float x[16];
-      scores(j, x);
+      scores(s0 + j, x);
 #pragma unroll
       for (int c = 0; c < 16; ++c) top = fmaxf(top, x[c]);
     }
-    raise(top);
-    const float ref = r.m == -INFINITY ? 0.f : r.m;
-    float l = 0.f;
+    if (!raise(C, i, 2 * it + h, top, w)) return false;
+    const float ref = w.r.m == -INFINITY ? 0.f : w.r.m;
 #pragma unroll 1
     for (int j = 0; j < kSubs / 2; ++j) {                      // P lies over scores that have been read
       float x[16], sum = 0.f;
-      scores(j, x);
+      scores(s0 + j, x);
       const uint32_t bad = bad_bits(s0 + j);
       uint32_t p[8];
 #pragma unroll
@@ -533,11 +575,12 @@ __device__ __forceinline__ void soft_half(const ChunkAttnArgs& A, ChunkCtrl& C, 
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) p[u] = pack_h2(x[2 * u], x[2 * u + 1]);
-      tc_st8(ts + 8 * j, p);
-      l = fmaf(sum, scaling(s0 + j).vinv, l);
+      tc_st8(w.ts + kHalf * h + 8 * j, p);
+      w.r.l = fmaf(sum, scaling(s0 + j).vinv, w.r.l);
     }
-    r.l += l;
+    hand_over_p(C, i, h);
   }
+  return true;
 }
 
 // Row r (m, l, O) of stream i -> the caller's output, or this split's partial.
@@ -582,62 +625,84 @@ __device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W,
   if (mine && partial) *reinterpret_cast<float2*>(A.ws_ml + 2 * slot) = make_float2(r.m, r.l);
 }
 
-// The softmax of stream i; this thread has row `row` of the stream's rows.
+__device__ __forceinline__ int thread_id() {   // read again where it is used, not held over the loop
+  int t;
+  asm volatile("mov.u32 %0, %tid.x;" : "=r"(t));
+  return t;
+}
+
+// The softmax of stream i (its warps 4i ... 4i + 3; a thread has the row of its
+// number), then the stream's part of the output.
 template <int FMT, bool SHARED>
-__device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& range, ChunkCtrl& C, int i, int row,
-                                       uint8_t* generic) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void soften(const ChunkAttnArgs& A, ChunkCtrl& C, int i, float* o1_rows) {
   const Work& W = C.work;
   const int tiles = W.stream_tiles[i];
-  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-  const uint32_t ts = tm_s(C.tmem, i) + lanes, to = tm_o(C.tmem, i) + lanes;
-  const int R = W.r0 + (SHARED ? i * kRows : 0) + row;
-  const bool idle = R - lane >= W.rows;                      // no row of this warp is real
-  RowState r{-INFINITY, 0.f};
   bool ok = true;
+  Row w;
+  w.r = RowState{-INFINITY, 0.f};
   {
-    const int last = W.rows - 1, n = W.sq.n, w0 = R - lane;
-    const int p_row = n + min(R, last) / W.gq;
-    const int p_lo = n + min(w0, last) / W.gq, p_hi = n + min(w0 + 31, last) / W.gq;
-    const float cm = fabsf(A.scale_log2) * C.qmul[SHARED ? i * kRows + row : row];
+    const int row = thread_id() % kRows, lane = row & 31;
+    const int R = W.r0 + (SHARED ? i * kRows : 0) + row, last = W.rows - 1, w0 = R - lane;
+    const bool idle = w0 > last;                             // no row of this warp is real
+    const uint32_t lanes = (uint32_t)(row & ~31) << 16;
+    w.ts = tm_s(C.tmem, i) + lanes;
+    w.to = tm_o(C.tmem, i) + lanes;
+    w.cm = fabsf(A.scale_log2) * C.qmul[SHARED ? i * kRows + row : row];
+    if (lane == 0)
+      C.seen[4 * i + row / 32] = make_int2(
+          A.window > 0 ? W.sq.n + min(w0 + 31, last) / W.gq - A.window + 1 : 0, W.sq.n + min(w0, last) / W.gq);
+    __syncwarp();
     Scaling packed{1.f, 0.f, 1.f};           // FP8 codes stand for themselves; the static scales come in here
     if (FMT == 8) {
       const float vs = fmaxf(A.c.fp8_scale[A.c.shape.num_kv_heads + W.kv], 0x1p-100f);
       packed = Scaling{A.c.fp8_scale[W.kv], log2f(vs), 1.f / vs};
     }
-    const int first = W.first;
-    for (int x = 0; x < 2 * tiles && ok; ++x) {
-      const int it = x >> 1, h = x & 1, g = SHARED ? it : 2 * it + i;
-      if (h == 0 && !(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
-      if (!idle) {
-        tc_after();
-        soft_half(A, C, i, x, C.info[g % kInfos], packed, range.tile(first + g) * kKeys + kHalf * h, kSubs / 2 * h, p_row,
-                  p_lo, p_hi, cm, ts + kHalf * h, to, r, ok);
-        tc_wait_st();
-        tc_before();
+    for (int it = 0; it < tiles; ++it) {
+      if (!(ok = warp_wait(&C.s_full[i], it & 1, &C.abort))) break;
+      if (idle) {
+        if ((thread_id() & 31) == 0) {
+          bar_arrive(&C.p_ready[i][0]);
+          bar_arrive(&C.p_ready[i][1]);
+        }
+        continue;
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(&C.p_ready[i][h]);
+      tc_after();
+      const int g = SHARED ? it : 2 * it + i, slot = g % kInfos;
+      const int t0 = W.range.tile(W.first + g) * kKeys;
+      const uint2 kinds = *reinterpret_cast<const uint2*>(C.info[slot].kind);
+      // warp-uniform: every token is visible to every row, and all have one scaling
+      const volatile int2& seen = C.seen[thread_id() / 32];
+      const bool plain = t0 + kKeys - 1 <= seen.y && (t0 >= seen.x || t0 + kKeys <= A.sinks) && kinds.x == kinds.y &&
+                         kinds.x == (kinds.x & 0xFFu) * 0x01010101u && (kinds.x & 0xFFu) != 2u;
+      if (plain) {
+        ok = soft_plain(C, i, it, FMT != 8 || (kinds.x & 0xFFu) == 0u ? packed : Scaling{1.f, 0.f, 1.f}, w);
+      } else {
+        const int R = W.r0 + (SHARED ? i * kRows : 0) + thread_id() % kRows;
+        ok = soft_any(A, C, i, it, slot, packed, t0, W.sq.n + min(R, W.rows - 1) / W.gq, w);
+      }
+      if (!ok) break;
     }
   }
   const bool any = tiles > 0;
   if (ok && any) ok = warp_wait(&C.finished[i], 0, &C.abort);
+  const int row = thread_id() % kRows, lane = row & 31, R = W.r0 + (SHARED ? i * kRows : 0) + row;
+  const bool idle = R - lane >= W.rows;
   tc_after();
   const float one[2] = {1.f, 0.f};
   if (SHARED) {
-    if (ok && !idle) store_row(A, W, R, r, to, any, nullptr, one);
+    if (ok && !idle) store_row(A, W, R, w.r, w.to, any, nullptr, one);
   } else {
     // join the streams: stream 1's row through shared memory (the tiles are used up)
-    float* o1 = reinterpret_cast<float*>(generic + kTileBytes16) + row * kHeadDim;
+    float* o1 = o1_rows + row * kHeadDim;
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     if (i == 1) {
-      C.ml[row][0] = r.m;
-      C.ml[row][1] = r.l;
+      C.ml[row][0] = w.r.m;
+      C.ml[row][1] = w.r.l;
       if (ok && any && !idle) {
 #pragma unroll 1
         for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
           float o[32];
-          tc_ld32(o, to + c0);
+          tc_ld32(o, w.to + c0);
           tc_wait_ld();
 #pragma unroll
           for (int u = 0; u < 8; ++u)
@@ -648,12 +713,12 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, const TileRange& 
     }
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     if (i == 0 && ok && !idle) {
-      const float m1 = C.ml[row][0], l1 = C.ml[row][1];
+      const float m0 = w.r.m, m1 = C.ml[row][0], l1 = C.ml[row][1];
       const bool two = W.stream_tiles[1] > 0;
-      const float M = fmaxf(r.m, m1), ref = M == -INFINITY ? 0.f : M;
-      const float f[2] = {ex2(r.m - ref), two && m1 != -INFINITY ? ex2(m1 - ref) : 0.f};
-      const RowState j{M, r.l * f[0] + (two ? l1 * f[1] : 0.f)};
-      store_row(A, W, R, j, to, any, two ? o1 : nullptr, f);
+      const float M = fmaxf(m0, m1), ref = M == -INFINITY ? 0.f : M;
+      const float f[2] = {ex2(m0 - ref), two && m1 != -INFINITY ? ex2(m1 - ref) : 0.f};
+      const RowState j{M, w.r.l * f[0] + (two ? l1 * f[1] : 0.f)};
+      store_row(A, W, R, j, w.to, any, two ? o1 : nullptr, f);
     }
   }
   tc_before();
@@ -682,6 +747,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
   if (W.r0 >= W.rows) return;
   const int block_rows = min(kBlockRows, W.rows - W.r0);
   const TileRange range(W.sq.n + W.r0 / W.gq, W.sq.n + (W.r0 + block_rows - 1) / W.gq, A.window, A.sinks, kKeys);
+  W.range = range;
   W.first = (int)((int64_t)range.count * W.split / A.splits);
   W.tiles = (int)((int64_t)range.count * (W.split + 1) / A.splits) - W.first;
   if (SHARED) {
@@ -708,6 +774,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     bar_init(&C.drained, 1);
     C.abort = 0;
     C.work = W;
+    C.clear = A.window > 0 ? W.sq.n + (W.r0 + block_rows - 1) / W.gq - A.window + 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kProducerWarp) {
@@ -755,10 +822,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     if (!issue_all<SHARED>(C, q_tiles, k_tiles, v_tiles) && elect_one()) drain(C);
     __syncwarp();
   } else if (warp >= kProducerWarp) {
-    produce<FMT, SHARED>(A, range, C, unit, k_tiles, v_tiles, warp - kProducerWarp);
+    produce<FMT, SHARED>(A, C, unit, k_tiles, v_tiles, warp - kProducerWarp);
   } else {
-    const int i = __shfl_sync(0xffffffffu, warp >> 2, 0), row = tid % kRows;   // warp-uniform for the compiler too
-    soften<FMT, SHARED>(A, range, C, i, row, generic);
+    soften<FMT, SHARED>(A, C, __shfl_sync(0xffffffffu, warp >> 2, 0), reinterpret_cast<float*>(generic + kTileBytes16));
   }
   __syncthreads();
   if (warp == kProducerWarp) {

@@ -49,6 +49,7 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkAttnArgs& A, int b) {
 // window to p1.  tile(i) for 0 <= i < count.
 struct TileRange {
   int lead, skip, count;
+  TileRange() = default;
   __device__ __forceinline__ TileRange(int p0, int p1, int window, int sinks, int TS) {
     const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
     skip = lo / TS;
