@@ -51,6 +51,8 @@ struct ChunkCtrl {
   double freq[kHeadDim / 2];                 // RoPE pair frequencies
   Work work;                                 // kept here, not in every thread's registers
   int clear;                                 // tokens from here on are hidden from no row of the CTA by the window
+  int sinks;                                 // tiles that end here or below neither
+  int straight;                              // quantized tokens whose codes go straight to halves (0: rotated or sparse keys)
   int2 seen[8];                              // the same for a softmax warp's rows, and its first row's position
 };
 
@@ -179,8 +181,8 @@ __device__ __forceinline__ uint32_t tm_o(uint32_t tmem, int i) { return tmem + 2
 // goes into `info`.  Returns its kind.  (A function of its own with few
 // arguments: its registers are not the fast path's.)
 template <int FMT>
-__device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, int base, uint32_t kt, uint32_t vt,
-                                          int sub, TileInfo& info) {
+__device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, const UnitSrc<FMT>& unit, int base,
+                                          uint32_t kt, uint32_t vt, int sub, TileInfo& info) {
   const kvq_cache& c = A.c;
   const kvq_shape& s = c.shape;
   const ChunkSeq& sq = C.work.sq;
@@ -196,19 +198,39 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
     zero_rows(vt, sub);
     bad = 1u << 16;
   } else {
+    if (quant == kTile && !rope && !s.sparse) {              // (a tile at the window's edge)
+      SubSrc p;
+      SubWords<FMT> w;
+      sub_src<FMT>(unit, base / kTile, p);
+      load_keys<FMT>(p, w);
+      load_values<FMT>(p, w);
+      if (!values_odd<FMT>(w)) {
+        if (FMT == 6 && p.two) {
+          keys_to_tile<FMT, 2>(w, kt, sub);
+          values_to_tile<FMT, 2>(w, vt, sub);
+        } else {
+          keys_to_tile<FMT, SubWords<FMT>::kBits>(w, kt, sub);
+          values_to_tile<FMT, SubWords<FMT>::kBits>(w, vt, sub);
+        }
+        return 0;
+      }
+    }
     const size_t ring = is_token_cache(FMT) ? 0 : Addr::ring_row(s, C.work.b, C.work.kv, 0);
     const size_t at = ((size_t)sq.t0 * s.num_kv_heads + C.work.kv) * kHeadDim;
-    const int64_t stride = (int64_t)s.num_kv_heads * kHeadDim;
-    const int slots = max(window_slots(s), 1);
-    const RawRows kr{(const uint16_t*)c.k_res + ring, A.k + at, stride, sq.n, sq.total, slots};
-    const RawRows vr{(const uint16_t*)c.v_res + ring, A.v + at, stride, sq.n, sq.total, slots};
-    if (quant == 0 && !rope) {
-      uint32_t none;
-      ek = rows_to_tile<true>(kr, base, kt, sub, none);
-      ev = rows_to_tile<false>(vr, base, vt, sub, bad);
-    } else {
-      ek = keys_any<FMT>(d, quant, kr, base, rope ? C.freq : nullptr, kt, sub);
-      ev = values_any<FMT>(d, quant, vr, base, vt, sub, bad);
+    RawRows raw;
+    raw.stride = (int64_t)s.num_kv_heads * kHeadDim;
+    raw.n = sq.n;
+    raw.total = sq.total;
+    raw.slots = max(window_slots(s), kTile);
+    raw.slot0 = base % raw.slots;
+#pragma unroll 1
+    for (int v = 0; v < 2; ++v) {                            // keys, then values
+      raw.ring = (const uint16_t*)(v ? c.v_res : c.k_res) + ring;
+      raw.fresh = (v ? A.v : A.k) + at;
+      if (quant != 0 || rope || !rows_to_tile(raw, base, v ? vt : kt, sub, v == 0)) {
+        if (v) ev = values_any<FMT>(d, quant, raw, base, vt, sub, bad);
+        else ek = keys_any<FMT>(d, quant, raw, base, rope ? C.freq : nullptr, kt, sub);
+      }
     }
   }
   if (ek == 0 && ev == 0 && bad == 0u) return FMT == 8 ? 1 : 0;
@@ -255,9 +277,8 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, co
   auto value_tile = [&](int x) { return v_tiles + (x / kSubs) % kValueStages * kTileBytes16; };
   auto packed = [&](int x, SubSrc& d) {
     const int t0 = tile(x) * kKeys, base = t0 + kTile * (x % kSubs);
-    // codes go straight to halves; tokens past `clear` and tiles of sinks hide from no row
-    return A.c.shape.rope_theta <= 0.f && !A.c.shape.sparse && W.sq.nq - base >= kTile &&
-           (t0 >= *(volatile int*)&C.clear || t0 + kKeys <= A.sinks) && sub_src<FMT>(unit, base / kTile, d);
+    const volatile ChunkCtrl& V = C;
+    return V.straight - base >= kTile && (t0 >= V.clear || t0 + kKeys <= V.sinks) && sub_src<FMT>(unit, base / kTile, d);
   };
 
   int x = pw;
@@ -269,7 +290,7 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, co
       // give their values first.
       if (!wait_keys(x) || !wait_values(x)) return;
       const int g = x / kSubs, sub = x % kSubs;
-      const int kind = produce_other<FMT>(A, C, tile(x) * kKeys + kTile * sub, key_tile(x), value_tile(x),
+      const int kind = produce_other<FMT>(A, C, unit, tile(x) * kKeys + kTile * sub, key_tile(x), value_tile(x),
                                           sub, C.info[g % kInfos]);
       if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
       hand_over(&C.k_full[g % kStages]);
@@ -500,10 +521,31 @@ __device__ __forceinline__ void hand_over_p(ChunkCtrl& C, int i, int h) {
   if ((threadIdx.x & 31) == 0) bar_arrive(&C.p_ready[i][h]);
 }
 
-// A tile whose tokens are all visible to every row of the warp and have one
-// scaling.  Two halves of 64 keys: a row's scores of a half are held in
+__device__ __forceinline__ int thread_id() {   // read again where it is used, not held over the loop
+  int t;
+  asm volatile("mov.u32 %0, %tid.x;" : "=r"(t));
+  return t;
+}
+
+// Bits t - t0 of the tokens in [t0, t0 + 64) that the row at position p sees, in
+// the tile's row order.
+__device__ __forceinline__ uint2 visible64(int t0, int p, int window, int sinks) {
+  auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+  unsigned long long m = below(p + 1 - t0);
+  if (window > 0) m &= ~below(p - window + 1 - t0) | below(sinks - t0);
+  m = (m & 0x9999999999999999ull) | ((m & 0x2222222222222222ull) << 1) | ((m & 0x4444444444444444ull) >> 1);
+  return make_uint2((uint32_t)m, (uint32_t)(m >> 32));
+}
+__device__ __forceinline__ void hide(float (&x)[32], uint32_t seen) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c) x[c] = seen >> c & 1u ? x[c] : -INFINITY;
+}
+
+// A tile whose tokens have one scaling (all: every row of the warp sees every
+// token).  Two halves of 64 keys: a row's scores of a half are held in
 // registers, and the second half's are on their way while the first is weighed.
-__device__ __forceinline__ bool soft_plain(ChunkCtrl& C, int i, int it, const Scaling& sc, Row& w) {
+__device__ __forceinline__ bool soft_plain(const ChunkAttnArgs& A, ChunkCtrl& C, int i, int it, bool all, int t0,
+                                           int first_row, const Scaling& sc, Row& w) {
   const float k = w.cm * sc.kmul;
   const pair_t k2 = pair(k, k);
   float xa[32], xb[32];
@@ -512,6 +554,12 @@ __device__ __forceinline__ bool soft_plain(ChunkCtrl& C, int i, int it, const Sc
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     tc_wait_ld();
+    if (!all) {
+      const int R = min(first_row + thread_id() % kRows, C.work.rows - 1);
+      const uint2 seen = visible64(t0 + kHalf * h, C.work.sq.n + R / C.work.gq, A.window, A.sinks);
+      hide(xa, seen.x);
+      hide(xb, seen.y);
+    }
     if (!raise(C, i, 2 * it + h, fmaf(most(most(-INFINITY, xa), xb), k, sc.vlog), w)) return false;
     const float off = sc.vlog - (w.r.m == -INFINITY ? 0.f : w.r.m);
     const pair_t off2 = pair(off, off);
@@ -625,12 +673,6 @@ __device__ __forceinline__ void store_row(const ChunkAttnArgs& A, const Work& W,
   if (mine && partial) *reinterpret_cast<float2*>(A.ws_ml + 2 * slot) = make_float2(r.m, r.l);
 }
 
-__device__ __forceinline__ int thread_id() {   // read again where it is used, not held over the loop
-  int t;
-  asm volatile("mov.u32 %0, %tid.x;" : "=r"(t));
-  return t;
-}
-
 // The softmax of stream i (its warps 4i ... 4i + 3; a thread has the row of its
 // number), then the stream's part of the output.
 template <int FMT, bool SHARED>
@@ -647,7 +689,8 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, ChunkCtrl& C, int
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
     w.ts = tm_s(C.tmem, i) + lanes;
     w.to = tm_o(C.tmem, i) + lanes;
-    w.cm = fabsf(A.scale_log2) * C.qmul[SHARED ? i * kRows + row : row];
+    // (not 0, so that -inf stays -inf: with a scale of 0 every score is the same all the same)
+    w.cm = fmaxf(fabsf(A.scale_log2), 0x1p-100f) * C.qmul[SHARED ? i * kRows + row : row];
     if (lane == 0)
       C.seen[4 * i + row / 32] = make_int2(
           A.window > 0 ? W.sq.n + min(w0 + 31, last) / W.gq - A.window + 1 : 0, W.sq.n + min(w0, last) / W.gq);
@@ -672,13 +715,14 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, ChunkCtrl& C, int
       }
       tc_after();
       const uint2 kinds = *reinterpret_cast<const uint2*>(C.info[slot].kind);
-      // warp-uniform: every token is visible to every row, and all have one scaling
-      const bool plain = clear && kinds.x == kinds.y && kinds.x == (kinds.x & 0xFFu) * 0x01010101u && (kinds.x & 0xFFu) != 2u;
-      if (plain) {
-        ok = soft_plain(C, i, it, FMT != 8 || (kinds.x & 0xFFu) == 0u ? packed : Scaling{1.f, 0.f, 1.f}, w);
+      const bool one = kinds.x == kinds.y && kinds.x == (kinds.x & 0xFFu) * 0x01010101u && (kinds.x & 0xFFu) != 2u;
+      const int first_row = W.r0 + (SHARED ? i * kRows : 0);
+      if (one) {
+        ok = soft_plain(A, C, i, it, clear, t0, first_row,
+                        FMT != 8 || (kinds.x & 0xFFu) == 0u ? packed : Scaling{1.f, 0.f, 1.f}, w);
       } else {
-        const int R = W.r0 + (SHARED ? i * kRows : 0) + thread_id() % kRows;
-        ok = soft_any(A, C, i, it, slot, packed, t0, W.sq.n + min(R, W.rows - 1) / W.gq, w);
+        const int R = min(first_row + thread_id() % kRows, W.rows - 1);
+        ok = soft_any(A, C, i, it, slot, packed, t0, W.sq.n + R / W.gq, w);
       }
       if (!ok) break;
     }
@@ -774,6 +818,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     bar_init(&C.drained, 1);
     C.abort = 0;
     C.work = W;
+    C.straight = s.rope_theta > 0.f || s.sparse ? 0 : W.sq.nq;
+    C.sinks = A.sinks;
     C.clear = A.window > 0 ? W.sq.n + (W.r0 + block_rows - 1) / W.gq - A.window + 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -787,30 +833,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     for (int i = lane; i < kHeadDim / 2; i += 32) C.freq[i] = pow((double)s.rope_theta, -2.0 * i / kHeadDim);
   }
   // Query rows -> fp16 in the key tiles' channel order, powers of two aside
-  // (they go into the row's factor), negated for a negative scale.
-  if (warp < 4 || (SHARED && warp < 8)) {
-    const int R = min(W.r0 + tid, W.rows - 1);               // rows past the end repeat the last one
-    const uint4* src = reinterpret_cast<const uint4*>(
-        A.q + ((size_t)(W.sq.t0 + R / W.gq) * s.num_q_heads + W.kv * W.gq + R % W.gq) * kHeadDim);
-    float amax = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      float x[8];
-      unpack8(src[i], x);
+  // (they go into the row's factor), negated for a negative scale; 16 threads
+  // a row, rows past the end zero.
+  {
+    constexpr int kPer = kBlockRows * 16 / kChunkThreads;
+    const int p = tid & 15;
+    uint4 w[kPer];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) amax = fmaxf(amax, finite_abs(x[u]));
+    for (int u = 0; u < kPer; ++u) {
+      const int R = W.r0 + (tid >> 4) + u * (kChunkThreads / 16);
+      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (R < W.rows)
+        w[u] = *reinterpret_cast<const uint4*>(
+            A.q + ((size_t)(W.sq.t0 + R / W.gq) * s.num_q_heads + W.kv * W.gq + R % W.gq) * kHeadDim + 8 * p);
     }
-    const int e = tile_exponent(amax);
-    const float sign = A.scale_log2 < 0.f ? -1.f : 1.f;
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      float x[8];
-      unpack8(src[i], x);
+    const uint32_t sign = A.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll 1
+    for (int u = 0; u < kPer; ++u) {
+      const int row = (tid >> 4) + u * (kChunkThreads / 16);
+      float x[8], amax = 0.f;
+      uint4 v = w[0];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = sign * (e ? scale_by(x[u], -e) : x[u]);
-      put_key8(q_tiles + (tid / kRows) * kTileBytes16, tid % kRows, i, x);
+      for (int i = 0; i + 1 < kPer; ++i) w[i] = w[i + 1];
+      v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
+      unpack8(v, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[i]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int e = tile_exponent(amax);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = e ? scale_by(x[i], -e) : x[i];
+      put_key8(q_tiles + (row / kRows) * kTileBytes16, row % kRows, p, x);
+      if (p == 0) C.qmul[row] = scale_by(1.f, e);
     }
-    C.qmul[tid] = scale_by(1.f, e);
     fence_async();
   }
   tc_before();

@@ -96,14 +96,6 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
   x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
 }
-__device__ __forceinline__ bool any_not_finite(const uint4& w) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bad = bad || (x[i] & 0x7F80u) == 0x7F80u || (x[i] & 0x7F800000u) == 0x7F800000u;
-  return bad;
-}
-
 // ---------------------------------------------------------------------------
 // Whole quantized subtiles: codes -> exact halves -> one fma per pair
 // ---------------------------------------------------------------------------
@@ -382,13 +374,69 @@ struct RawRows {
   const uint16_t* ring;        // slot 0 of the unit's ring
   const uint16_t* fresh;       // the chunk's row of token n for this head
   int64_t stride;              // between chunk rows
-  int n, total, slots;
-  __device__ __forceinline__ uint4 load(int t, int p) const {
-    if (t < n) return *reinterpret_cast<const uint4*>(ring + (size_t)(t % slots) * kHeadDim + 8 * p);
-    if (t < total) return *reinterpret_cast<const uint4*>(fresh + (t - n) * stride + 8 * p);
-    return make_uint4(0u, 0u, 0u, 0u);
+  int n, total, slots;         // (slots >= 16)
+  int slot0;                   // slot of token base
+  // Piece p (8 channels) of row r; t = base + r.
+  __device__ __forceinline__ uint4 load(int t, int r, int p) const {
+    int slot = slot0 + r;
+    if (slot >= slots) slot -= slots;
+    const uint16_t* src = t < n ? ring + (size_t)slot * kHeadDim : fresh + (t - n) * stride;
+    return t < total ? *reinterpret_cast<const uint4*>(src + 8 * p) : make_uint4(0u, 0u, 0u, 0u);
   }
 };
+
+// Largest of two packed pairs of bf16 magnitudes (sign bits cleared; the bit
+// patterns are in order, infinities and NaN on top).
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+__device__ __forceinline__ uint32_t abs_max8(uint32_t m, const uint4& w) {
+  return abs_max2(abs_max2(abs_max2(abs_max2(m, w.x), w.y), w.z), w.w);
+}
+__device__ __forceinline__ uint32_t larger_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+
+// Eight bf16 numbers -> four fp16 pairs, in the key tiles' channel order or in order.
+__device__ __forceinline__ void put_raw8(uint32_t at, const uint4& w, bool key) {
+  const float x0 = bf16_lo(w.x), x1 = bf16_hi(w.x), x2 = bf16_lo(w.y), x3 = bf16_hi(w.y);
+  const float x4 = bf16_lo(w.z), x5 = bf16_hi(w.z), x6 = bf16_lo(w.w), x7 = bf16_hi(w.w);
+  st_shared16(at, pack_h2(x0, key ? x4 : x1), pack_h2(key ? x1 : x2, key ? x5 : x3),
+              pack_h2(key ? x2 : x4, key ? x6 : x5), pack_h2(key ? x3 : x6, x7));
+}
+
+// Sixteen bf16 rows (keys or values) into a tile.  False, and nothing written,
+// if a number is not finite or the magnitudes need a power of two taken out.
+__device__ __forceinline__ bool rows_to_tile(const RawRows& raw, int base, uint32_t tile, int sub, bool key) {
+  const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
+  uint4 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = raw.load(base + 2 * i + half, 2 * i + half, p);
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = abs_max8(m, w[i]);
+  m = __reduce_max_sync(0xffffffffu, larger_half(m));
+  if (m != 0u && (m < 0x3C80u || m >= 0x4700u)) return false;      // outside [2^-6, 2^15)
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    put_raw8(piece_at(tile, kTile * sub + 4 * (i >> 1) + 2 * half + (i & 1), p), w[i], key);
+  return true;
+}
+
+// Whether a value of the subtile could be anything but a finite half (its
+// scale and zero are large, or it holds an e4m3 NaN): to be looked at closely
+// where a row may not see it, since 0 times such a value is NaN.
+template <int FMT>
+__device__ __forceinline__ bool values_odd(const SubWords<FMT>& w) {
+  uint32_t odd = 0u;
+  if constexpr (FMT == 8) {
+#pragma unroll
+    for (int i = 0; i < SubWords<FMT>::kVW; ++i) odd |= ((w.v[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  } else {
+    // |zero| >= 2^15, or scale >= 2^11 (INT8: 2^7): below both, code * scale + zero < 65504
+    constexpr uint32_t top = FMT == 16 ? 0x5800u : 0x6800u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      odd |= ((w.vm[q] & 0x7FFF7FFFu) + (((0x8000u - 0x7800u) << 16) | (0x8000u - top))) & 0x80008000u;
+  }
+  return __any_sync(0xffffffffu, odd != 0u);
+}
 
 __device__ __forceinline__ void rope8(float (&x)[8], int t, int ch, const double* freq) {
 #pragma unroll
@@ -405,7 +453,7 @@ __device__ __forceinline__ void rope8(float (&x)[8], int t, int ch, const double
 // packed tile d, the others raw.  Two passes (largest magnitude, then the
 // rows), so that any range of numbers fits.  Returns the power of two taken out.
 template <int FMT>
-__device__ __forceinline__ int keys_any(const TileSrc& d, int quant, const RawRows& raw, int base, const double* freq,
+__device__ __noinline__ int keys_any(const TileSrc& d, int quant, const RawRows& raw, int base, const double* freq,
                                      uint32_t tile, int sub) {
   const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
   float amax = 0.f;
@@ -430,7 +478,7 @@ __device__ __forceinline__ int keys_any(const TileSrc& d, int quant, const RawRo
     if (quant > 0) key_rows<FMT>(d, 0, quant, one);
     for (int r = quant + half; r < kTile; r += 2) {
       float x[8];
-      unpack8(raw.load(base + r, p), x);
+      unpack8(raw.load(base + r, r, p), x);
       one(r, 8 * p, x);
     }
     if (pass == 0) e = tile_exponent(warp_max(amax) * (freq ? 1.5f : 1.f));   // a rotation grows a pair by sqrt 2 at most
@@ -441,7 +489,7 @@ __device__ __forceinline__ int keys_any(const TileSrc& d, int quant, const RawRo
 // Values alike; rows with a value that is not finite become zero and set
 // their tile row's bit in `bad`.
 template <int FMT>
-__device__ __forceinline__ int values_any(const TileSrc& d, int quant, const RawRows& raw, int base, uint32_t tile, int sub,
+__device__ __noinline__ int values_any(const TileSrc& d, int quant, const RawRows& raw, int base, uint32_t tile, int sub,
                                        uint32_t& bad) {
   const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
   float amax = 0.f;
@@ -470,7 +518,7 @@ __device__ __forceinline__ int values_any(const TileSrc& d, int quant, const Raw
     if (quant > 0) value_rows<FMT>(d, 0, quant, one);
     for (int r = quant + half; r < kTile; r += 2) {
       float x[8];
-      unpack8(raw.load(base + r, p), x);
+      unpack8(raw.load(base + r, r, p), x);
       one(r, 8 * p, x);
     }
     if (pass == 0) {
@@ -480,64 +528,6 @@ __device__ __forceinline__ int values_any(const TileSrc& d, int quant, const Raw
   }
   bad = 0u;
   for (int r = 0; r < kTile; ++r) bad |= (mine >> r & 1u) << row_of_token(r);
-  return e;
-}
-
-// Sixteen bf16 rows (keys or values) in one pass over memory.
-template <bool KEY>
-__device__ __forceinline__ int rows_to_tile(const RawRows& raw, int base, uint32_t tile, int sub, uint32_t& bad) {
-  const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
-  uint4 w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = raw.load(base + 2 * i + half, p);
-  bad = 0u;
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float x[8];
-    unpack8(w[i], x);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(x[u]));
-  }
-  amax = warp_max(amax);                         // fmaxf drops NaN
-  // rows with numbers that are not finite (seldom): dropped one by one
-  bool odd = !(amax < INFINITY);
-  if constexpr (!KEY) {
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) nan = nan || any_not_finite(w[i]);
-    odd = __any_sync(0xffffffffu, nan);
-  }
-  if (odd) {
-    amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x[8];
-      unpack8(w[i], x);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) amax = fmaxf(amax, finite_abs(x[u]));
-      if constexpr (!KEY) {
-        const uint32_t b = __ballot_sync(0xffffffffu, any_not_finite(w[i]));
-        if (b & 0xFFFFu) bad |= 1u << row_of_token(2 * i);
-        if (b >> 16) bad |= 1u << row_of_token(2 * i + 1);
-        if (half ? b >> 16 : b & 0xFFFFu) w[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    amax = warp_max(amax);
-  }
-  const int e = tile_exponent(amax);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float x[8];
-    unpack8(w[i], x);
-    if (e != 0) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = scale_by(x[u], -e);
-    }
-    const int r = kTile * sub + 4 * (i >> 1) + 2 * half + (i & 1);
-    if (KEY) put_key8(tile, r, p, x);
-    else put_value8(tile, r, p, x);
-  }
   return e;
 }
 
