@@ -15,7 +15,7 @@ namespace kvq {
 
 constexpr int kRows = 128;                   // query rows per stream: one TMEM lane and one softmax thread each
 constexpr int kProducerWarp = 8;             // warps 0-3 and 4-7: softmax of streams 0 and 1; 8-14: producers
-constexpr int kProducers = 7;
+constexpr int kProducers = 7;                // (and the softmax warps none of whose rows is real)
 constexpr int kMmaWarp = kProducerWarp + kProducers;            // issues every product
 constexpr int kChunkThreads = 32 * (kMmaWarp + 1);              // four warps per scheduler: 128 registers each
 constexpr int kHalf = kKeys / 2;             // a row's softmax takes 64 keys at a time
@@ -223,15 +223,21 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
     raw.total = sq.total;
     raw.slots = max(window_slots(s), kTile);
     raw.slot0 = base % raw.slots;
-#pragma unroll 1
-    for (int v = 0; v < 2; ++v) {                            // keys, then values
-      raw.ring = (const uint16_t*)(v ? c.v_res : c.k_res) + ring;
-      raw.fresh = (v ? A.v : A.k) + at;
-      if (quant != 0 || rope || !rows_to_tile(raw, base, v ? vt : kt, sub, v == 0)) {
-        if (v) ev = values_any<FMT>(d, quant, raw, base, vt, sub, bad);
-        else ek = keys_any<FMT>(d, quant, raw, base, rope ? C.freq : nullptr, kt, sub);
-      }
+    RawRows raw_v = raw;
+    raw.ring = (const uint16_t*)c.k_res + ring;
+    raw.fresh = A.k + at;
+    raw_v.ring = (const uint16_t*)c.v_res + ring;
+    raw_v.fresh = A.v + at;
+    bool k_done = false, v_done = false;
+    if (quant == 0 && !rope) {
+      RawWords x[2];                                         // both on their way at once
+      load_rows(raw, base, x[0]);
+      load_rows(raw_v, base, x[1]);
+      k_done = rows_to_tile(x[0], kt, sub, true);
+      v_done = rows_to_tile(x[1], vt, sub, false);
     }
+    if (!k_done) ek = keys_any<FMT>(d, quant, raw, base, rope ? C.freq : nullptr, kt, sub);
+    if (!v_done) ev = values_any<FMT>(d, quant, raw_v, base, vt, sub, bad);
   }
   if (ek == 0 && ev == 0 && bad == 0u) return FMT == 8 ? 1 : 0;
   if (lane == 0) {
@@ -243,14 +249,15 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
   return 2;
 }
 
-// Producer warp pw: every seventh subtile (subtile x is number x % 8 of tile
-// x / 8).  In a run of whole quantized subtiles the keys are one subtile ahead
-// of the values, K(x) K(x + 7) V(x) K(x + 14) V(x + 7) ..., so that a tile's last
-// keys do not wait for the stage of its first values, and packed words are on
-// their way while others are turned into halves.  Any other subtile is made on
+// Producer pw of `step`: subtiles pw, pw + step, ... (subtile x is number x % 8
+// of tile x / 8).  In a run of whole quantized subtiles the keys are one
+// subtile ahead of the values, K(x) K(x + step) V(x) K(x + 2 step) V(x + step)
+// ..., so that a tile's last keys do not wait for the stage of its first
+// values, and packed words are on their way while others are turned into
+// halves.  Any other subtile is made on
 // its own between two runs, when no word is held.
 template <int FMT, bool SHARED>
-__device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, const UnitSrc<FMT>& unit, uint32_t k_tiles, uint32_t v_tiles, int pw) {
+__device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, const UnitSrc<FMT>& unit, uint32_t k_tiles, uint32_t v_tiles, int pw, int step) {
   constexpr int kValueStages = value_stages(SHARED);
   const int lane = threadIdx.x & 31;
   const volatile Work& W = C.work;           // read where it is used: registers are short
@@ -295,13 +302,13 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, co
       if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
       hand_over(&C.k_full[g % kStages]);
       hand_over(&C.v_full[g % kValueStages]);
-      x += kProducers;
+      x += step;
       continue;
     }
     SubWords<FMT> w;
     load_keys<FMT>(d, w);
     bool more, two = false;                  // two: the held values have 2-bit codes
-    for (int y = -1;; y = x, x += kProducers) {
+    for (int y = -1;; y = x, x += step) {
       // keys of x
       const int g = x / kSubs;
       if (!wait_keys(x)) return;
@@ -311,7 +318,7 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, co
       if (lane == 0) C.info[g % kInfos].kind[x % kSubs] = 0;
       hand_over(&C.k_full[g % kStages]);
       const SubSrc here = d;
-      more = x + kProducers < last && packed(x + kProducers, d);
+      more = x + step < last && packed(x + step, d);
       if (more) load_keys<FMT>(d, w);
       // values of y, the subtile before
       if (y >= 0) {
@@ -328,7 +335,7 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, co
     if (FMT == 6 && two) values_to_tile<FMT, 2>(w, value_tile(x), x % kSubs);
     else values_to_tile<FMT, SubWords<FMT>::kBits>(w, value_tile(x), x % kSubs);
     hand_over(&C.v_full[(x / kSubs) % kValueStages]);
-    x += kProducers;
+    x += step;
   }
 }
 
@@ -737,8 +744,10 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, ChunkCtrl& C, int
     if (ok && !idle) store_row(A, W, R, w.r, w.to, any, nullptr, one);
   } else {
     // join the streams: stream 1's row through shared memory (the tiles are used up)
+    const int threads = 64 * min(4, (W.rows - W.r0 + 31) / 32);      // the softmax warps of both streams
+    auto join = [&] { asm volatile("bar.sync 1, %0;\n" ::"r"(threads) : "memory"); };
     float* o1 = o1_rows + row * kHeadDim;
-    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    join();
     if (i == 1) {
       C.ml[row][0] = w.r.m;
       C.ml[row][1] = w.r.l;
@@ -755,7 +764,7 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, ChunkCtrl& C, int
         }
       }
     }
-    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    join();
     if (i == 0 && ok && !idle) {
       const float m0 = w.r.m, m1 = C.ml[row][0], l1 = C.ml[row][1];
       const bool two = W.stream_tiles[1] > 0;
@@ -813,7 +822,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     for (int i = 0; i < kMaxValueStages; ++i) { bar_init(&C.v_full[i], kSubs); bar_init(&C.v_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       bar_init(&C.s_full[i], 1); bar_init(&C.o_done[i], 1); bar_init(&C.finished[i], 1);
-      bar_init(&C.p_ready[i][0], 4); bar_init(&C.p_ready[i][1], 4);
+      const int busy = SHARED ? 4 : (block_rows + 31) / 32;
+      bar_init(&C.p_ready[i][0], busy); bar_init(&C.p_ready[i][1], busy);
     }
     bar_init(&C.drained, 1);
     C.abort = 0;
@@ -877,10 +887,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
   if (warp == kMmaWarp) {
     if (!issue_all<SHARED>(C, q_tiles, k_tiles, v_tiles) && elect_one()) drain(C);
     __syncwarp();
-  } else if (warp >= kProducerWarp) {
-    produce<FMT, SHARED>(A, C, unit, k_tiles, v_tiles, warp - kProducerWarp);
-  } else {
+  } else if (warp < kProducerWarp && (SHARED || 32 * (warp & 3) < block_rows)) {
     soften<FMT, SHARED>(A, C, __shfl_sync(0xffffffffu, warp >> 2, 0), reinterpret_cast<float*>(generic + kTileBytes16));
+  } else {
+    // with shared keys every softmax warp stays one; otherwise those without rows help
+    const int busy = SHARED ? 4 : (block_rows + 31) / 32;    // softmax warps per stream
+    const int pw = warp >= kProducerWarp ? warp - kProducerWarp
+                                         : kProducers + (warp >> 2) * (4 - busy) + (warp & 3) - busy;
+    produce<FMT, SHARED>(A, C, unit, k_tiles, v_tiles, pw, kProducers + 2 * (4 - busy));
   }
   __syncthreads();
   if (warp == kProducerWarp) {

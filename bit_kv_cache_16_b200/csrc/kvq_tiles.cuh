@@ -401,21 +401,27 @@ __device__ __forceinline__ void put_raw8(uint32_t at, const uint4& w, bool key) 
               pack_h2(key ? x2 : x4, key ? x6 : x5), pack_h2(key ? x3 : x6, x7));
 }
 
-// Sixteen bf16 rows (keys or values) into a tile.  False, and nothing written,
-// if a number is not finite or the magnitudes need a power of two taken out.
-__device__ __forceinline__ bool rows_to_tile(const RawRows& raw, int base, uint32_t tile, int sub, bool key) {
-  const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
+// Sixteen bf16 rows, as loaded (piece lane % 16 of rows 2i + lane / 16), into a
+// tile.  False, and nothing written, if a number is not finite or the
+// magnitudes need a power of two taken out.
+struct RawWords {
   uint4 w[8];
+};
+__device__ __forceinline__ void load_rows(const RawRows& raw, int base, RawWords& x) {
+  const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = raw.load(base + 2 * i + half, 2 * i + half, p);
+  for (int i = 0; i < 8; ++i) x.w[i] = raw.load(base + 2 * i + half, 2 * i + half, p);
+}
+__device__ __forceinline__ bool rows_to_tile(const RawWords& x, uint32_t tile, int sub, bool key) {
+  const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
   uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = abs_max8(m, w[i]);
+  for (int i = 0; i < 8; ++i) m = abs_max8(m, x.w[i]);
   m = __reduce_max_sync(0xffffffffu, larger_half(m));
   if (m != 0u && (m < 0x3C80u || m >= 0x4700u)) return false;      // outside [2^-6, 2^15)
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    put_raw8(piece_at(tile, kTile * sub + 4 * (i >> 1) + 2 * half + (i & 1), p), w[i], key);
+    put_raw8(piece_at(tile, kTile * sub + 4 * (i >> 1) + 2 * half + (i & 1), p), x.w[i], key);
   return true;
 }
 
