@@ -85,6 +85,13 @@ static_assert(kWarps * 8 * kMergeStride * 4 <= kWarps * kFp8Stages * Stage<8>::k
 
 constexpr float kLn2 = 0.69314718055994531f;   // ln 2: log2 units -> natural-log units
 
+constexpr float kHeadroom = 13.f;   // WIN: the weights' reference lies this far (log2) below the largest
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The visible tokens of a windowed decode (WIN): the last `window` (0: all)
 // and the first `sinks` of every sequence.
 struct WindowSpec {
@@ -530,7 +537,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFp8MinBlocks) decode_fp8_kernel(
     }
     const float tmax = fmaxf(fmaxf(fmaxf(S2[0][0][0], S2[0][0][1]), fmaxf(S2[0][1][0], S2[0][1][1])),
                              fmaxf(fmaxf(S2[1][0][0], S2[1][0][1]), fmaxf(S2[1][1][0], S2[1][1][1])));
-    online_max_update(quad_max(tmax), st, O);
+    online_max_update(quad_max(tmax) - (WIN ? kHeadroom : 0.f), st, O);
 #pragma unroll
     for (int tt = 0; tt < 2; ++tt) {
       if (tt == 0 || nt == 2) {
@@ -673,10 +680,22 @@ __device__ __forceinline__ float aprep_int(const uint8_t* km_smem, const uint4* 
 // converter give the A fragment of m-tile ww directly: row g = channel a,
 // row g + 8 = channel b, k = tokens.  INT2/INT4 values come out as
 // code * 2^-9 (the accumulators hold 2^-9 times their sums; INT8 does not).
-template <int FMT, bool WIDE>
+// MID: the codes are taken about the middle of their range (value_middle; the
+// caller adds it to the zero points), exactly: over a long axis sum p s code is
+// large against the output, and the tensor core's accumulation, which cuts
+// off, would leave up to 3e-4 of it (measured at 65000 INT8 tokens; 1e-6 so).
+template <int FMT> __device__ __forceinline__ float value_middle() { return FMT == 16 ? 128.f : FMT == 4 ? 7.5f : 1.5f; }
+template <int FMT, bool WIDE, bool MID>
 __device__ __forceinline__ void pv_tile_int(const uint8_t* vt, uint32_t b0, uint32_t b1, uint32_t c0, uint32_t c1,
                                             float (&O)[8][4]) {
   const int lane = threadIdx.x & 31;
+  auto byte_h2 = [](uint32_t x) {              // 1024 + code -> code (- 128)
+    return MID ? hfma2(x, 0x3C003C00u, 0xE480E480u) : unmagic<1>(x);
+  };
+  auto middle = [](uint32_t x) {               // code 2^-9 -> (code - middle) 2^-9
+    constexpr uint32_t m = FMT == 4 ? 0xA380A380u : 0x9A009A00u;      // -7.5 2^-9, -1.5 2^-9
+    return MID ? hfma2(x, 0x3C003C00u, m) : x;
+  };
   if constexpr (FMT == 16) {
     // INT8: word j of this lane holds channel 16g + j of tokens 2l, 2l+1,
     // 2l+8, 2l+9 (one byte each); m-tile mt takes words 2mt (row g) and
@@ -689,10 +708,10 @@ __device__ __forceinline__ void pv_tile_int(const uint8_t* vt, uint32_t b0, uint
       for (int h = 0; h < 2; ++h) {
         const int mt = 2 * i + h;
         const uint32_t wa = w[2 * h], wb = w[2 * h + 1];
-        const uint32_t a0 = unmagic<1>(prmt(wa, 0x64646464u, 0x4140u));
-        const uint32_t a1 = unmagic<1>(prmt(wb, 0x64646464u, 0x4140u));
-        const uint32_t a2 = unmagic<1>(prmt(wa, 0x64646464u, 0x4342u));
-        const uint32_t a3 = unmagic<1>(prmt(wb, 0x64646464u, 0x4342u));
+        const uint32_t a0 = byte_h2(prmt(wa, 0x64646464u, 0x4140u));
+        const uint32_t a1 = byte_h2(prmt(wb, 0x64646464u, 0x4140u));
+        const uint32_t a2 = byte_h2(prmt(wa, 0x64646464u, 0x4342u));
+        const uint32_t a3 = byte_h2(prmt(wb, 0x64646464u, 0x4342u));
         mma_f16(O[mt], a0, a1, a2, a3, b0, b1);
         if (WIDE) mma_f16(O[mt], a0, a1, a2, a3, c0, c1);
       }
@@ -707,6 +726,7 @@ __device__ __forceinline__ void pv_tile_int(const uint8_t* vt, uint32_t b0, uint
       uint32_t a0, a1, a2, a3;
       e4m3x4_to_h2x2(w[ww] & 0x0F0F0F0Fu, a0, a2);
       e4m3x4_to_h2x2((w[ww] >> 4) & 0x0F0F0F0Fu, a1, a3);
+      a0 = middle(a0); a1 = middle(a1); a2 = middle(a2); a3 = middle(a3);
       mma_f16(O[ww], a0, a1, a2, a3, b0, b1);
       if (WIDE) mma_f16(O[ww], a0, a1, a2, a3, c0, c1);
     }
@@ -722,6 +742,7 @@ __device__ __forceinline__ void pv_tile_int(const uint8_t* vt, uint32_t b0, uint
         uint32_t a0, a1, a2, a3;
         e4m3x4_to_h2x2((w[ww] >> (4 * h)) & 0x03030303u, a0, a2);
         e4m3x4_to_h2x2((w[ww] >> (4 * h + 2)) & 0x03030303u, a1, a3);
+        a0 = middle(a0); a1 = middle(a1); a2 = middle(a2); a3 = middle(a3);
         mma_f16(O[2 * ww + h], a0, a1, a2, a3, b0, b1);
         if (WIDE) mma_f16(O[2 * ww + h], a0, a1, a2, a3, c0, c1);
       }
@@ -851,7 +872,7 @@ __device__ __forceinline__ void window_chunk_int(const kvq_cache& c, int b, int 
       S[nt][e] = (g < gq && tok < r && vis.token(nq + tok)) ? (a0[e] + a1[e]) * scale_log2 : -INFINITY;
     }
   }
-  int_max_update(quad_max(fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[1][0], S[1][1]))), st, O, hc0);
+  int_max_update(quad_max(fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[1][0], S[1][1]))) - (WIN ? kHeadroom : 0.f), st, O, hc0);
   const float mref = st.m == -INFINITY ? 0.f : st.m;
   float p[2][2];
 #pragma unroll
@@ -1466,6 +1487,11 @@ __global__ void __launch_bounds__(kIntWarps * 32, KVQ_DECODE_INT_MIN_BLOCKS) dec
             }
           }
           const f2_t p01 = f2(pr[0][0], pr[0][1]), p89 = f2(pr[1][0], pr[1][1]);
+          if constexpr (WIN) {                         // codes are taken about their middle (pv_tile_int)
+            const f2_t mid = f2(value_middle<F>(), value_middle<F>());
+            z01 = f2_fma(s01, mid, z01);
+            z89 = f2_fma(s89, mid, z89);
+          }
           float za, zb;
           f2_split(f2_fma(p01, z01, f2_mul(p89, z89)), za, zb);
           st.z += za + zb;
@@ -1476,7 +1502,7 @@ __global__ void __launch_bounds__(kIntWarps * 32, KVQ_DECODE_INT_MIN_BLOCKS) dec
           split_h2(x0, x1, hi0, lo0);
           split_h2(x8, x9, hi1, lo1);
           pv_operands<WIDE>(hi0, lo0, hi1, lo1, b0, b1, c0, c1);
-          pv_tile_int<F, WIDE>(sbuf + SF::kV + tt * SF::kTB, b0, b1, c0, c1, O);
+          pv_tile_int<F, WIDE, WIN>(sbuf + SF::kV + tt * SF::kTB, b0, b1, c0, c1, O);
         };
           // dense-and-sparse: the kept keys' share of the scores,
         // q[h][c] (k_c - z_c) for the token each channel kept (its dense
@@ -1530,6 +1556,25 @@ __global__ void __launch_bounds__(kIntWarps * 32, KVQ_DECODE_INT_MIN_BLOCKS) dec
           return fmaxf(fmaxf(fmaxf(S0[0][0], S0[0][1]), fmaxf(S0[1][0], S0[1][1])),
                        fmaxf(fmaxf(S1[0][0], S1[0][1]), fmaxf(S1[1][0], S1[1][1])));
         };
+      // What the running maximum has to cover.  WIN: scores plus log2 of the
+      // value scales, less kHeadroom, so that p s uses fp16's whole range: p s
+      // <= 2^kHeadroom, and its low half is a normal number down to 2^-16 of
+      // the largest (p alone stays below 2^(kHeadroom + 24), s >= 2^-24).
+      auto reference = [&](const float (&S0)[2][2], const float (&S1)[2][2], int nt) {
+          if constexpr (!WIN) return chunk_max(S0, S1);
+          float top = -INFINITY;
+          for (int tt = 0; tt < nt; ++tt) {
+            const uint8_t* vm = sbuf + SF::kVm + tt * 64;
+#pragma unroll
+            for (int n8 = 0; n8 < 2; ++n8) {
+              const uint2 m = *reinterpret_cast<const uint2*>(vm + 32 * n8 + 8 * l);
+              const float (&S)[2][2] = tt ? S1 : S0;
+              top = fmaxf(top, S[n8][0] + lg2(fmaxf(__low2float(u32_as_h2(m.x)), 0x1p-24f)));
+              top = fmaxf(top, S[n8][1] + lg2(fmaxf(__low2float(u32_as_h2(m.y)), 0x1p-24f)));
+            }
+          }
+          return top - kHeadroom;
+      };
         float S0[2][2], S1[2][2];
         if constexpr (ROPE) {
           // Keys stored before RoPE: dequantize k^ = code * s + z in fp32,
@@ -1627,7 +1672,7 @@ __global__ void __launch_bounds__(kIntWarps * 32, KVQ_DECODE_INT_MIN_BLOCKS) dec
           }
           hide(0, S0);
           hide(1, S1);
-          int_max_update(quad_max(chunk_max(S0, S1)), st, O, hc0);
+          int_max_update(quad_max(reference(S0, S1, nt)), st, O, hc0);
           pv_softmax_tile(0, S0);
           if (nt == 2) pv_softmax_tile(1, S1);
         } else if constexpr (F == 16) {
@@ -1658,7 +1703,7 @@ __global__ void __launch_bounds__(kIntWarps * 32, KVQ_DECODE_INT_MIN_BLOCKS) dec
           else S1[0][0] = S1[0][1] = S1[1][0] = S1[1][1] = -INFINITY;
           hide(0, S0);
           hide(1, S1);
-          int_max_update(quad_max(chunk_max(S0, S1)), st, O, hc0);
+          int_max_update(quad_max(reference(S0, S1, nt)), st, O, hc0);
           pv_softmax_tile(0, S0, ulen - t0 * kTile);
           if (nt == 2) pv_softmax_tile(1, S1, ulen - (t0 + 1) * kTile);
         } else if (T > 1 && nt == 2) {
@@ -1669,7 +1714,7 @@ __global__ void __launch_bounds__(kIntWarps * 32, KVQ_DECODE_INT_MIN_BLOCKS) dec
           k_sparse_fix(S0, S1);
           hide(0, S0);
           hide(1, S1);
-          int_max_update(quad_max(chunk_max(S0, S1)), st, O, hc0, SP ? vcorr : nullptr, gq);
+          int_max_update(quad_max(reference(S0, S1, nt)), st, O, hc0, SP ? vcorr : nullptr, gq);
           pv_softmax_tile(0, S0);
           pv_softmax_tile(1, S1);
         } else {
@@ -1686,7 +1731,7 @@ __global__ void __launch_bounds__(kIntWarps * 32, KVQ_DECODE_INT_MIN_BLOCKS) dec
           k_sparse_fix(S0, S1);
           hide(0, S0);
           hide(1, S1);
-          int_max_update(quad_max(chunk_max(S0, S1)), st, O, hc0, SP ? vcorr : nullptr, gq);
+          int_max_update(quad_max(reference(S0, S1, nt)), st, O, hc0, SP ? vcorr : nullptr, gq);
           pv_softmax_tile(0, S0);
           if (nt == 2) pv_softmax_tile(1, S1);
         }
