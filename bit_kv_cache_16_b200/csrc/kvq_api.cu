@@ -19,9 +19,9 @@ cudaError_t launch_decode(const kvq_cache& c, const void* q, float* out, float* 
 cudaError_t launch_merge(const float* outs, const float* lses, int parts, long long rows, float* out, float* lse_out,
                          cudaStream_t st);
 cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v, const uint8_t* cls,
-                                const int32_t* cu, int max_new, cudaStream_t st);
-cudaError_t launch_read_tokens(const kvq_cache& c, const int32_t* start, const int32_t* cu, int max_len, void* k,
-                               void* v, cudaStream_t st);
+                                const int32_t* cu, int total, int max_new, cudaStream_t st);
+cudaError_t launch_read_tokens(const kvq_cache& c, const int32_t* start, const int32_t* cu, int rows, int max_len,
+                               void* k, void* v, cudaStream_t st);
 cudaError_t launch_chunk_attention(const ChunkAttnArgs& A, cudaStream_t st);
 int chunk_default_splits(const kvq_shape& s, int rows, int max_new, int max_len, int window, int sinks);
 size_t chunk_workspace_bytes(const kvq_shape& s, int num_splits, int rows);
@@ -242,28 +242,30 @@ kvq_status kvq_append_flush_mixed(kvq_cache* cache, const void* k_new_bf16, cons
 }
 
 kvq_status kvq_append_chunk(kvq_cache* cache, const void* k_new_bf16, const void* v_new_bf16,
-                            const uint8_t* token_class_dev, const int32_t* cu_seqlens_dev, int32_t max_new,
-                            kvq_stream_t stream) {
+                            const uint8_t* token_class_dev, const int32_t* cu_seqlens_dev, int32_t total_new,
+                            int32_t max_new, kvq_stream_t stream) {
   kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
-  if (!cu_seqlens_dev || max_new < 0) return KVQ_ERR_INVALID_ARG;
+  if (!cu_seqlens_dev || total_new < 0 || max_new < 0) return KVQ_ERR_INVALID_ARG;
   const bool mixed = is_mixed(cache->shape.format);
-  if (max_new > 0 && (!k_new_bf16 || !v_new_bf16 || (mixed && !token_class_dev))) return KVQ_ERR_INVALID_ARG;
+  if (total_new > 0 && max_new > 0 && (!k_new_bf16 || !v_new_bf16 || (mixed && !token_class_dev))) return KVQ_ERR_INVALID_ARG;
   if (!mixed && token_class_dev) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(k_new_bf16) || !aligned16(v_new_bf16) || ((uintptr_t)cu_seqlens_dev & 3u)) return KVQ_ERR_ALIGNMENT;
   return from_cuda(
-      launch_append_chunk(*cache, k_new_bf16, v_new_bf16, token_class_dev, cu_seqlens_dev, max_new, (cudaStream_t)stream));
+      launch_append_chunk(*cache, k_new_bf16, v_new_bf16, token_class_dev, cu_seqlens_dev, total_new,
+                          min(max_new, total_new), (cudaStream_t)stream));
 }
 
 kvq_status kvq_read_tokens(const kvq_cache* cache, const int32_t* start_dev, const int32_t* cu_seqlens_dev,
-                           int32_t max_len, void* k_bf16, void* v_bf16, kvq_stream_t stream) {
+                           int32_t total, int32_t max_len, void* k_bf16, void* v_bf16, kvq_stream_t stream) {
   kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
-  if (!cu_seqlens_dev || max_len < 0 || (max_len > 0 && !k_bf16 && !v_bf16)) return KVQ_ERR_INVALID_ARG;
+  if (!cu_seqlens_dev || total < 0 || max_len < 0) return KVQ_ERR_INVALID_ARG;
+  if (total > 0 && max_len > 0 && !k_bf16 && !v_bf16) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(k_bf16) || !aligned16(v_bf16) || ((uintptr_t)cu_seqlens_dev & 3u) || ((uintptr_t)start_dev & 3u))
     return KVQ_ERR_ALIGNMENT;
   return from_cuda(
-      launch_read_tokens(*cache, start_dev, cu_seqlens_dev, max_len, k_bf16, v_bf16, (cudaStream_t)stream));
+      launch_read_tokens(*cache, start_dev, cu_seqlens_dev, total, max_len, k_bf16, v_bf16, (cudaStream_t)stream));
 }
 
 // Split count of a chunk attention call (0 = the library's choice), or 0 if

@@ -18,7 +18,7 @@ struct ChunkPlan {
 };
 
 // Every thread of the block calls this and gets the same plan.
-__device__ __forceinline__ ChunkPlan chunk_plan(const kvq_cache& c, const int32_t* cu, int b, int max_new) {
+__device__ __forceinline__ ChunkPlan chunk_plan(const kvq_cache& c, const int32_t* cu, int b, int total, int max_new) {
   const kvq_shape& s = c.shape;
   ChunkPlan p;
   p.t0 = cu[b];
@@ -27,7 +27,7 @@ __device__ __forceinline__ ChunkPlan chunk_plan(const kvq_cache& c, const int32_
   p.nq = c.n_quant[b];
   p.err = 0u;
   if (state_bad(s, p.n, p.nq)) p.err = KVQ_DEVERR_STATE;
-  else if (p.m < 0 || p.m > max_new) p.err = KVQ_DEVERR_PREFILL_LEN;
+  else if (p.m < 0 || p.m > max_new || p.t0 < 0 || p.t0 > total - p.m) p.err = KVQ_DEVERR_PREFILL_LEN;
   else if (p.m > s.capacity - p.n) p.err = KVQ_DEVERR_APPEND_FULL;
   if (p.err) p.m = 0;
   p.n1 = p.n + p.m;
@@ -75,12 +75,13 @@ __device__ __forceinline__ void ring_put(const kvq_cache& c, const uint16_t* k, 
 template <int FMT, int G, bool SPARSE>
 __global__ void __launch_bounds__(128, SPARSE ? 5 : (G <= 32 ? 6 : 5))
     append_chunk_int_kernel(kvq_cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                            const uint8_t* __restrict__ cls, const int32_t* __restrict__ cu, int max_new, int groups) {
+                            const uint8_t* __restrict__ cls, const int32_t* __restrict__ cu, int total, int max_new,
+                            int groups) {
   grid_dependents_launch();   // the commit kernel may be scheduled; it waits for this grid
   const kvq_shape& s = c.shape;
   const int item = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int Ws = window_slots(s);
-  const ChunkPlan p = chunk_plan(c, cu, b, max_new);
+  const ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
   if (p.err && item == 0 && h == 0 && tid == 0) set_err(c.err_word, p.err);
   const int lo = max(p.n, p.nq1);                    // new window tokens: [lo, n1)
   if (item >= groups) {
@@ -174,11 +175,11 @@ __device__ __forceinline__ void fp8_token_tile(const uint16_t* rows, int64_t str
 template <bool I8>
 __global__ void __launch_bounds__(128, I8 ? 6 : 8)
     append_chunk_token_kernel(kvq_cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                              const int32_t* __restrict__ cu, int max_new) {
+                              const int32_t* __restrict__ cu, int total, int max_new) {
   grid_dependents_launch();
   const kvq_shape& s = c.shape;
   const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5;
-  const ChunkPlan p = chunk_plan(c, cu, b, max_new);
+  const ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
   if (p.err && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) set_err(c.err_word, p.err);
   const int tile = p.n / kTile + 2 * blockIdx.x + (warp & 1);
   if (p.m == 0 || tile * kTile >= p.n1) return;
@@ -202,11 +203,12 @@ __global__ void __launch_bounds__(128, I8 ? 6 : 8)
 // Grid (B), 128 threads: after the chunk kernel, the window classes (MIXED)
 // and the counters of every sequence whose chunk was taken.
 __global__ void __launch_bounds__(128) append_chunk_commit_kernel(kvq_cache c, const uint8_t* __restrict__ cls,
-                                                                  const int32_t* __restrict__ cu, int max_new) {
+                                                                  const int32_t* __restrict__ cu, int total,
+                                                                  int max_new) {
   grid_dependency_wait();     // every CTA of the chunk kernel has read the state
   const kvq_shape& s = c.shape;
   const int b = blockIdx.x;
-  const ChunkPlan p = chunk_plan(c, cu, b, max_new);
+  const ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
   if (p.err) return;
   if (is_mixed(s.format)) {
     const int Ws = window_slots(s);
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(128) append_chunk_commit_kernel(kvq_cache c, c
 }
 
 cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v, const uint8_t* cls,
-                                const int32_t* cu, int max_new, cudaStream_t st) {
+                                const int32_t* cu, int total, int max_new, cudaStream_t st) {
   const kvq_shape& s = c.shape;
   const uint16_t* kk = (const uint16_t*)k;
   const uint16_t* vv = (const uint16_t*)v;
@@ -230,8 +232,8 @@ cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v
     // a chunk of m tokens touches at most (m + 30) / 16 tiles
     dim3 grid(((most + 2 * kTile - 2) / kTile + 1) / 2, s.num_kv_heads, s.batch);
     if (grid.x == 0) grid.x = 1;
-    if (is_int8(s.format)) append_chunk_token_kernel<true><<<grid, 128, 0, st>>>(c, kk, vv, cu, max_new);
-    else append_chunk_token_kernel<false><<<grid, 128, 0, st>>>(c, kk, vv, cu, max_new);
+    if (is_int8(s.format)) append_chunk_token_kernel<true><<<grid, 128, 0, st>>>(c, kk, vv, cu, total, max_new);
+    else append_chunk_token_kernel<false><<<grid, 128, 0, st>>>(c, kk, vv, cu, total, max_new);
   } else {
     // n - nq <= R + G and nq1 <= n1 - R: at most (G + m) / G groups; the new
     // window tokens are at most m and at most R + G
@@ -240,7 +242,7 @@ cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v
     dim3 grid(groups + tail, s.num_kv_heads, s.batch);
 #define KVQ_CHUNK_CASE(B, GG, SP) \
   if (s.format == B && s.group == GG && (bool)s.sparse == SP) \
-    append_chunk_int_kernel<B, GG, SP><<<grid, 128, 0, st>>>(c, kk, vv, cls, cu, max_new, groups);
+    append_chunk_int_kernel<B, GG, SP><<<grid, 128, 0, st>>>(c, kk, vv, cls, cu, total, max_new, groups);
     KVQ_CHUNK_CASE(4, 16, false) KVQ_CHUNK_CASE(4, 32, false) KVQ_CHUNK_CASE(4, 64, false)
     KVQ_CHUNK_CASE(4, 128, false) KVQ_CHUNK_CASE(2, 16, false) KVQ_CHUNK_CASE(2, 32, false)
     KVQ_CHUNK_CASE(2, 64, false) KVQ_CHUNK_CASE(2, 128, false) KVQ_CHUNK_CASE(4, 16, true)
@@ -258,7 +260,7 @@ cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v
   pdl_attribute(attr[0]);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_chunk_commit_kernel, c, cls, cu, max_new);
+  return cudaLaunchKernelEx(&cfg, append_chunk_commit_kernel, c, cls, cu, total, max_new);
 }
 
 }  // namespace kvq

@@ -9,6 +9,7 @@ struct ReadArgs {
   const int32_t* cu;       // [B + 1] output rows
   uint16_t* k;             // bf16 [rows][H_kv][128], or null
   uint16_t* v;             // same, or null
+  int rows;                // of k and v
   int max_len;
 };
 
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(128) read_tokens_kernel(ReadArgs A) {
     if (lead) atomicOr(c.err_word, KVQ_DEVERR_STATE);
     return;
   }
-  if (len < 0 || len > A.max_len || first < 0 || first > n || len > n - first) {
+  if (len < 0 || len > A.max_len || row0 < 0 || row0 > A.rows - len || first < 0 || first > n || len > n - first) {
     if (lead) atomicOr(c.err_word, KVQ_DEVERR_PREFILL_LEN);
     return;
   }
@@ -64,10 +65,10 @@ __global__ void __launch_bounds__(128) read_tokens_kernel(ReadArgs A) {
   else value_rows<FMT>(d, lo, hi, put);
 }
 
-cudaError_t launch_read_tokens(const kvq_cache& c, const int32_t* start, const int32_t* cu, int max_len, void* k,
-                               void* v, cudaStream_t st) {
+cudaError_t launch_read_tokens(const kvq_cache& c, const int32_t* start, const int32_t* cu, int rows, int max_len,
+                               void* k, void* v, cudaStream_t st) {
   const kvq_shape& s = c.shape;
-  const ReadArgs A{c, start, cu, (uint16_t*)k, (uint16_t*)v, max_len};
+  const ReadArgs A{c, start, cu, (uint16_t*)k, (uint16_t*)v, rows, max_len};
   const int most = min(max_len, s.capacity);         // longer ranges are rejected on the device
   // a range of m tokens touches at most (m + 30) / 16 tiles
   dim3 grid(((most + 2 * kTile - 2) / kTile + 1) / 2, s.num_kv_heads, s.batch);

@@ -7,7 +7,6 @@ of the library fails loudly: there is no CPU fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -89,8 +88,8 @@ def load(path: Optional[str] = None):
         "kvq_quantize_prefill_mixed": (i32, [pc, vp, vp, vp, vp, i32, vp]),
         "kvq_append_token_mixed": (i32, [pc, vp, vp, vp, vp]),
         "kvq_append_flush_mixed": (i32, [pc, vp, vp, vp, vp]),
-        "kvq_append_chunk": (i32, [pc, vp, vp, vp, vp, i32, vp]),
-        "kvq_read_tokens": (i32, [pc, vp, vp, i32, vp, vp, vp]),
+        "kvq_append_chunk": (i32, [pc, vp, vp, vp, vp, i32, i32, vp]),
+        "kvq_read_tokens": (i32, [pc, vp, vp, i32, i32, vp, vp, vp]),
         "kvq_chunk_attention": (i32, [pc, vp, vp, vp, vp, i32, i32, f32, i32, i32, vp, vp, sz, i32, i32, vp]),
         "kvq_chunk_workspace_bytes": (sz, [pc, i32, i32, i32, i32, i32, i32]),
         "kvq_decode_attention_window": (i32, [pc, vp, vp, vp, f32, i32, i32, vp, sz, i32, i32, vp]),
@@ -125,6 +124,11 @@ def _ptr(t) -> ctypes.c_void_p:
     if isinstance(t, int):
         return ctypes.c_void_p(t)
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _addr(t):
+    """Address for a pointer argument (ctypes takes the number; None is NULL)."""
+    return None if t is None else t if isinstance(t, int) else t.data_ptr()
 
 
 def _check(fn: str, status: int):
@@ -191,18 +195,19 @@ def kvq_append_flush_mixed(cache: KvqCache, k_new, v_new, token_class, stream=No
                                                                    _ptr(token_class), _stream(stream)))
 
 
-def kvq_append_chunk(cache: KvqCache, k_new, v_new, token_class, cu_seqlens, max_new: int, stream=None):
+def kvq_append_chunk(cache: KvqCache, k_new, v_new, token_class, cu_seqlens, total_new: int, max_new: int,
+                     stream=None):
     """Append a ragged chunk of new tokens (token_class: MIXED only, else None)."""
     _check("kvq_append_chunk",
-           load().kvq_append_chunk(ctypes.byref(cache), _ptr(k_new), _ptr(v_new), _ptr(token_class),
-                                   _ptr(cu_seqlens), int(max_new), _stream(stream)))
+           load().kvq_append_chunk(ctypes.byref(cache), _addr(k_new), _addr(v_new), _addr(token_class),
+                                   _addr(cu_seqlens), int(total_new), int(max_new), _stream(stream)))
 
 
-def kvq_read_tokens(cache: KvqCache, start, cu_seqlens, max_len: int, k_out, v_out, stream=None):
+def kvq_read_tokens(cache: KvqCache, start, cu_seqlens, total: int, max_len: int, k_out, v_out, stream=None):
     """Token ranges of the cache as bf16 rows (start None: from token 0; k_out or v_out None: not read)."""
     _check("kvq_read_tokens",
-           load().kvq_read_tokens(ctypes.byref(cache), _ptr(start), _ptr(cu_seqlens), int(max_len), _ptr(k_out),
-                                  _ptr(v_out), _stream(stream)))
+           load().kvq_read_tokens(ctypes.byref(cache), _addr(start), _addr(cu_seqlens), int(total), int(max_len),
+                                  _addr(k_out), _addr(v_out), _stream(stream)))
 
 
 def kvq_chunk_attention(cache: KvqCache, q, k_new, v_new, cu_seqlens, total_new: int, max_new: int,
@@ -210,9 +215,9 @@ def kvq_chunk_attention(cache: KvqCache, q, k_new, v_new, cu_seqlens, total_new:
                         num_splits: int, max_len: int, stream=None):
     """A chunk of new tokens attends to the cache and, causally, to itself."""
     _check("kvq_chunk_attention",
-           load().kvq_chunk_attention(ctypes.byref(cache), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cu_seqlens),
+           load().kvq_chunk_attention(ctypes.byref(cache), _addr(q), _addr(k_new), _addr(v_new), _addr(cu_seqlens),
                                       int(total_new), int(max_new), float(softmax_scale), int(window), int(sinks),
-                                      _ptr(out), _ptr(workspace), int(ws_bytes), int(num_splits), int(max_len),
+                                      _addr(out), _addr(workspace), int(ws_bytes), int(num_splits), int(max_len),
                                       _stream(stream)))
 
 
@@ -226,8 +231,8 @@ def kvq_decode_attention_window(cache: KvqCache, q, out, lse, softmax_scale: flo
                                 workspace, ws_bytes: int, num_splits: int, max_len: int, stream=None):
     """Decode over the last `window` tokens and the first `sinks` (lse None: not written)."""
     _check("kvq_decode_attention_window",
-           load().kvq_decode_attention_window(ctypes.byref(cache), _ptr(q), _ptr(out), _ptr(lse),
-                                              float(softmax_scale), int(window), int(sinks), _ptr(workspace),
+           load().kvq_decode_attention_window(ctypes.byref(cache), _addr(q), _addr(out), _addr(lse),
+                                              float(softmax_scale), int(window), int(sinks), _addr(workspace),
                                               int(ws_bytes), int(num_splits), int(max_len), _stream(stream)))
 
 
@@ -290,6 +295,11 @@ def kvq_read_error(cache: KvqCache, stream=None) -> int:
 # A cache whose buffers are torch device tensors
 # --------------------------------------------------------------------------
 
+# accepted types: bf16 rows may come as their bit patterns
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_INT32, _UINT8, _FLOAT = (torch.int32,), (torch.uint8,), (torch.float32,)
+
+
 class Cache:
     """Allocates every region of a cache (torch uint8 tensors on `device`)
     and keeps the C descriptor pointing at them."""
@@ -303,11 +313,18 @@ class Cache:
                               page_size, max_pages_per_seq, num_pages, float(rope_theta), int(sparse))
         self.device = torch.device(device)
         self.buffers = {}
+        # seq_len and n_quant side by side (each 16-byte aligned), so that reset() is one launch
+        n = max(kvq_buffer_bytes(self.shape, REGIONS.index("seq_len")), 16)
+        self._counters = torch.zeros(2, (n + 15) // 16 * 16, dtype=torch.uint8, device=self.device)
         for i, name in enumerate(REGIONS):
-            n = kvq_buffer_bytes(self.shape, i)
+            if name in ("seq_len", "n_quant"):
+                self.buffers[name] = self._counters[0 if name == "seq_len" else 1, :n]
+                continue
+            n_bytes = kvq_buffer_bytes(self.shape, i)
             # torch's caching allocator hands out 256-byte aligned blocks
-            t = torch.zeros(max(n, 16), dtype=torch.uint8, device=self.device) if n else None
+            t = torch.zeros(max(n_bytes, 16), dtype=torch.uint8, device=self.device) if n_bytes else None
             self.buffers[name] = t
+        self._index = self._counters.get_device()
         self.desc = KvqCache(self.shape, *[self.buffers[n].data_ptr() if self.buffers[n] is not None else None
                                            for n in REGIONS])
 
@@ -355,65 +372,67 @@ class Cache:
     def append_flush_mixed(self, k_new, v_new, token_class, stream=None):
         kvq_append_flush_mixed(self.desc, k_new, v_new, token_class, stream)
 
-    # The calls below check their tensors (device, element size, layout and
-    # shape) and run on the cache's device, whatever the current one is.
+    # The calls below check their tensors (device, type, layout and shape) and
+    # run on the cache's device, whatever the current one is.
 
-    def _need(self, name: str, t, shape, itemsize: int):
-        """t is a contiguous tensor on the cache's device, of this element size and shape (None: any extent)."""
-        if t.device.type != self.device.type or (self.device.index is not None and t.device != self.device):
+    def _need(self, name: str, t, rows, tail, dtypes):
+        """t is a contiguous tensor [rows, *tail] (rows None: any number) of one of these types on the cache's device."""
+        shape = t.shape
+        if (t.dtype in dtypes and shape[1:] == tail and (rows is None or shape[0] == rows) and
+                len(shape) == 1 + len(tail) and t.get_device() == self._index and t.is_contiguous()):
+            return
+        if t.get_device() != self._index:
             raise ValueError("%s is on %s, the cache on %s" % (name, t.device, self.device))
-        if t.element_size() != itemsize:
-            raise ValueError("%s has elements of %d bytes, not %d" % (name, t.element_size(), itemsize))
-        if not t.is_contiguous():
+        if t.dtype not in dtypes:
+            raise ValueError("%s is %s, not %s" % (name, t.dtype, dtypes[0]))
+        if len(shape) == 1 + len(tail) and shape[1:] == tail and (rows is None or shape[0] == rows):
             raise ValueError("%s is not contiguous" % name)
-        if len(shape) != t.dim() or any(e is not None and e != d for e, d in zip(shape, t.shape)):
-            raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape),
-                                                         tuple("*" if e is None else e for e in shape)))
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(shape), ("*" if rows is None else rows,) + tail))
 
     def _bytes_of(self, workspace) -> int:
         """Bytes of a workspace tensor (contiguous, on the cache's device) or 0 for None."""
         if workspace is None:
             return 0
-        self._need("workspace", workspace, tuple(workspace.shape), workspace.element_size())
+        if workspace.get_device() != self._index or not workspace.is_contiguous():
+            raise ValueError("workspace is on %s or not contiguous (the cache is on %s)" % (workspace.device, self.device))
         return workspace.numel() * workspace.element_size()
 
-    def _guard(self, stream):
-        """(a context in which the cache's device is current, the stream to use)."""
-        dev = self.buffers["seq_len"].device
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        return (contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)), stream
+    def _call(self, fn, stream, *args):
+        """fn(descriptor, *args, stream) with the cache's device current, on its current stream unless one is given."""
+        if torch.cuda.current_device() == self._index:
+            return fn(self.desc, *args, torch.cuda.current_stream() if stream is None else stream)
+        with torch.cuda.device(self._index):
+            return fn(self.desc, *args, torch.cuda.current_stream() if stream is None else stream)
 
     def reset(self):
         """Empty the cache: every sequence has no token (the FP8 scales stay)."""
-        self.seq_len().zero_()
-        self.n_quant().zero_()
+        self._counters.zero_()
 
     def append_chunk(self, k_new, v_new, cu_seqlens, max_new: int, token_class=None, stream=None):
-        """Append a ragged chunk: k_new, v_new bf16 [T, H_kv, 128], cu_seqlens int32 [B + 1]."""
+        """Append a ragged chunk: k_new, v_new bf16 [T, H_kv, 128], cu_seqlens int32 [B + 1]; token_class uint8 [T] for a
+        MIXED cache."""
         s = self.shape
-        self._need("k_new", k_new, (None, s.num_kv_heads, 128), 2)
-        self._need("v_new", v_new, tuple(k_new.shape), 2)
-        self._need("cu_seqlens", cu_seqlens, (s.batch + 1,), 4)
+        tail = (s.num_kv_heads, 128)
+        self._need("k_new", k_new, None, tail, _BF16)
+        self._need("v_new", v_new, k_new.shape[0], tail, _BF16)
+        self._need("cu_seqlens", cu_seqlens, s.batch + 1, (), _INT32)
         if token_class is not None:
-            self._need("token_class", token_class, (k_new.shape[0],), 1)
-        ctx, stream = self._guard(stream)
-        with ctx:
-            kvq_append_chunk(self.desc, k_new, v_new, token_class, cu_seqlens, max_new, stream)
+            self._need("token_class", token_class, k_new.shape[0], (), _UINT8)
+        self._call(kvq_append_chunk, stream, k_new, v_new, token_class, cu_seqlens, k_new.shape[0], max_new)
 
     def read_tokens(self, start, cu_seqlens, max_len: int, k_out, v_out, stream=None):
         """Tokens [start, start + length) of every sequence as bf16 rows [T, H_kv, 128] (start None: 0; either output
         may be None)."""
         s = self.shape
         if start is not None:
-            self._need("start", start, (s.batch,), 4)
-        self._need("cu_seqlens", cu_seqlens, (s.batch + 1,), 4)
+            self._need("start", start, s.batch, (), _INT32)
+        self._need("cu_seqlens", cu_seqlens, s.batch + 1, (), _INT32)
+        rows = None
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is not None:
-                self._need(name, t, (None, s.num_kv_heads, 128), 2)
-        ctx, stream = self._guard(stream)
-        with ctx:
-            kvq_read_tokens(self.desc, start, cu_seqlens, max_len, k_out, v_out, stream)
+                self._need(name, t, rows, (s.num_kv_heads, 128), _BF16)
+                rows = t.shape[0]
+        self._call(kvq_read_tokens, stream, start, cu_seqlens, 0 if rows is None else rows, max_len, k_out, v_out)
 
     def chunk_workspace_bytes(self, num_splits: int, total_new: int, max_new: int, max_len: int, window: int = 0,
                               sinks: int = 0) -> int:
@@ -424,16 +443,13 @@ class Cache:
         """out bf16 [T, H_q, 128]: the chunk's queries q over the cached tokens and, causally, over k_new, v_new."""
         s = self.shape
         rows = q.shape[0]
-        self._need("q", q, (None, s.num_q_heads, 128), 2)
-        self._need("k_new", k_new, (rows, s.num_kv_heads, 128), 2)
-        self._need("v_new", v_new, (rows, s.num_kv_heads, 128), 2)
-        self._need("out", out, (rows, s.num_q_heads, 128), 2)
-        self._need("cu_seqlens", cu_seqlens, (s.batch + 1,), 4)
-        n = self._bytes_of(workspace)
-        ctx, stream = self._guard(stream)
-        with ctx:
-            kvq_chunk_attention(self.desc, q, k_new, v_new, cu_seqlens, rows, max_new, softmax_scale, window, sinks,
-                                out, workspace, n, num_splits, max_len, stream)
+        self._need("q", q, None, (s.num_q_heads, 128), _BF16)
+        self._need("k_new", k_new, rows, (s.num_kv_heads, 128), _BF16)
+        self._need("v_new", v_new, rows, (s.num_kv_heads, 128), _BF16)
+        self._need("out", out, rows, (s.num_q_heads, 128), _BF16)
+        self._need("cu_seqlens", cu_seqlens, s.batch + 1, (), _INT32)
+        self._call(kvq_chunk_attention, stream, q, k_new, v_new, cu_seqlens, rows, max_new, softmax_scale, window, sinks,
+                   out, workspace, self._bytes_of(workspace), num_splits, max_len)
 
     def window_workspace_bytes(self, num_splits: int, max_len: int, window: int, sinks: int = 0) -> int:
         return kvq_window_workspace_bytes(self.desc, num_splits, max_len, window, sinks)
@@ -442,15 +458,12 @@ class Cache:
                                 num_splits: int, max_len: int, lse=None, stream=None):
         """out float [B, H_q, 128]: one query per sequence over its last `window` tokens and its first `sinks`."""
         s = self.shape
-        self._need("q", q, (s.batch, s.num_q_heads, 128), 2)
-        self._need("out", out, (s.batch, s.num_q_heads, 128), 4)
+        self._need("q", q, s.batch, (s.num_q_heads, 128), _BF16)
+        self._need("out", out, s.batch, (s.num_q_heads, 128), _FLOAT)
         if lse is not None:
-            self._need("lse", lse, (s.batch, s.num_q_heads), 4)
-        n = self._bytes_of(workspace)
-        ctx, stream = self._guard(stream)
-        with ctx:
-            kvq_decode_attention_window(self.desc, q, out, lse, softmax_scale, window, sinks, workspace, n, num_splits,
-                                        max_len, stream)
+            self._need("lse", lse, s.batch, (s.num_q_heads,), _FLOAT)
+        self._call(kvq_decode_attention_window, stream, q, out, lse, softmax_scale, window, sinks, workspace,
+                   self._bytes_of(workspace), num_splits, max_len)
 
     def workspace_bytes(self, num_splits: int, max_len: int) -> int:
         return kvq_decode_workspace_bytes(self.desc, num_splits, max_len)

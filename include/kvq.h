@@ -395,24 +395,26 @@ kvq_status kvq_merge_partials(const float *outs, const float *lses, int32_t part
  * leave (section 3.2 of the arganzheng page): seq_len += m,
  * n_quant = G*floor(max(seq_len - R, 0)/G) (seq_len for FP8 and INT8), with
  * the same codes, scales and window slots, bit for bit.
- *  k_new_bf16, v_new_bf16: bf16 [T_total][H_kv][D], the sequences' chunks
- *                  back to back; may be NULL when max_new is 0.
- *  token_class_dev: MIXED: uint8 [T_total], as kvq_quantize_prefill_mixed;
+ *  k_new_bf16, v_new_bf16: bf16 [total_new][H_kv][D], the sequences' chunks
+ *                  back to back; may be NULL when there are none.
+ *  token_class_dev: MIXED: uint8 [total_new], as kvq_quantize_prefill_mixed;
  *                  NULL for every other format.
  *  cu_seqlens_dev: int32 [B+1] device array, sequence b's chunk is rows
  *                  [cu[b], cu[b+1]); chunks may be empty.
+ *  total_new:      rows of k_new and v_new (and entries of token_class_dev).
  *  max_new:        an upper bound of the chunk lengths (sizes the grid).
  * FP8 encodes with the stored scales (saturating): they must be set, by an
  * earlier prefill or by the caller.  A sequence's chunk is dropped whole, its
- * state left as it was, if it is longer than max_new (KVQ_DEVERR_PREFILL_LEN),
+ * state left as it was, if it is longer than max_new or outside [0, total_new)
+ * (KVQ_DEVERR_PREFILL_LEN),
  * does not fit the capacity (KVQ_DEVERR_APPEND_FULL), needs a page whose id is
  * out of range (KVQ_DEVERR_PAGE_RANGE) or finds an inconsistent state
  * (KVQ_DEVERR_STATE).  Two launches; the second (counters) waits for the
  * first on the device.
  */
 kvq_status kvq_append_chunk(kvq_cache *cache, const void *k_new_bf16, const void *v_new_bf16,
-                            const uint8_t *token_class_dev, const int32_t *cu_seqlens_dev, int32_t max_new,
-                            kvq_stream_t stream);
+                            const uint8_t *token_class_dev, const int32_t *cu_seqlens_dev, int32_t total_new,
+                            int32_t max_new, kvq_stream_t stream);
 
 /*
  * Read cached tokens back as bf16 rows: x^ = code * scale + zero in fp32 (the
@@ -422,15 +424,17 @@ kvq_status kvq_append_chunk(kvq_cache *cache, const void *k_new_bf16, const void
  *  start_dev:      int32 [B] first token per sequence, or NULL (token 0).
  *  cu_seqlens_dev: int32 [B+1]; output rows [cu[b], cu[b+1]) receive tokens
  *                  start[b], start[b] + 1, ... of sequence b.
+ *  total:          rows of k_bf16 and v_bf16.
  *  max_len:        an upper bound of the range lengths (sizes the grid).
- *  k_bf16, v_bf16: bf16 [T_total][H_kv][D]; either may be NULL (not read).
- * A range that is negative, longer than max_len or passes seq_len[b] sets
+ *  k_bf16, v_bf16: bf16 [total][H_kv][D]; either may be NULL (not read).
+ * A range that is negative, longer than max_len, outside the total rows or
+ * past seq_len[b] sets
  * KVQ_DEVERR_PREFILL_LEN, a bad page id KVQ_DEVERR_PAGE_RANGE (its 16 rows),
  * an inconsistent state KVQ_DEVERR_STATE; the rows concerned, like rows that
  * belong to no range, are left as they were.  One launch.
  */
 kvq_status kvq_read_tokens(const kvq_cache *cache, const int32_t *start_dev, const int32_t *cu_seqlens_dev,
-                           int32_t max_len, void *k_bf16, void *v_bf16, kvq_stream_t stream);
+                           int32_t total, int32_t max_len, void *k_bf16, void *v_bf16, kvq_stream_t stream);
 
 /*
  * Attention of a chunk of new tokens over the packed cache and, causally,

@@ -20,8 +20,8 @@ def lib():
 def call(lib, name, cache, **kw):
     """The entry point with aligned dummy arguments, some replaced."""
     args = {
-        "kvq_append_chunk": dict(k=16, v=16, cls=None, cu=16, max_new=8, stream=None),
-        "kvq_read_tokens": dict(start=16, cu=16, max_len=8, k=16, v=16, stream=None),
+        "kvq_append_chunk": dict(k=16, v=16, cls=None, cu=16, total_new=8, max_new=8, stream=None),
+        "kvq_read_tokens": dict(start=16, cu=16, total=8, max_len=8, k=16, v=16, stream=None),
         "kvq_chunk_attention": dict(q=16, k=16, v=16, cu=16, total_new=8, max_new=8, scale=1.0, window=0, sinks=0,
                                     out=16, ws=16, ws_bytes=1 << 40, splits=0, max_len=8192, stream=None),
         "kvq_decode_attention_window": dict(q=16, out=16, lse=16, scale=1.0, window=64, sinks=4, ws=16,
@@ -34,7 +34,8 @@ def call(lib, name, cache, **kw):
 @pytest.mark.parametrize("name,kw,status", [
     ("kvq_append_chunk", dict(k=None), BAD), ("kvq_append_chunk", dict(v=None), BAD),
     ("kvq_append_chunk", dict(cu=None), BAD), ("kvq_append_chunk", dict(max_new=-1), BAD),
-    ("kvq_append_chunk", dict(cls=16), BAD), ("kvq_append_chunk", dict(k=24), ALIGN),
+    ("kvq_append_chunk", dict(cls=16), BAD), ("kvq_append_chunk", dict(total_new=-1), BAD),
+    ("kvq_read_tokens", dict(total=-1), BAD), ("kvq_append_chunk", dict(k=24), ALIGN),
     ("kvq_append_chunk", dict(cu=18), ALIGN),
     ("kvq_read_tokens", dict(cu=None), BAD), ("kvq_read_tokens", dict(max_len=-1), BAD),
     ("kvq_read_tokens", dict(k=None, v=None), BAD), ("kvq_read_tokens", dict(v=24), ALIGN),
@@ -105,6 +106,7 @@ class _Stub(kvq.Cache):
     def __init__(self):
         self.shape = _shape()
         self.device = torch.device("cpu")
+        self._index = -1
         self.desc = _fake_cache(self.shape)
 
 

@@ -208,6 +208,25 @@ def test_append_chunk_dropped():
     assert before.cap == cap
 
 
+def test_rows_outside_the_arrays():
+    """Offsets that leave the given rows drop that sequence: nothing is read or written outside."""
+    case = Case(4, [50, 60], [10, 4], seed=15).fill()
+    k = torch.zeros(10, 2, 128, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 7, 12], dtype=torch.int32, device="cuda")          # rows 10 and 11 do not exist
+    case.cache.append_chunk(k, k, cu, 10)
+    assert case.cache.error() == kvq.KVQ_DEVERR_PREFILL_LEN
+    assert GpuState(case.cache).seq_len[:2].tolist() == [57, 60]
+    case.cache.clear_error()
+    case.cache.append_chunk(k, k, torch.tensor([-3, 2, 4], dtype=torch.int32, device="cuda"), 10)
+    assert case.cache.error() == kvq.KVQ_DEVERR_PREFILL_LEN
+    assert GpuState(case.cache).seq_len[:2].tolist() == [57, 62]
+    case.cache.clear_error()
+    out = [torch.full((14, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    case.cache.read_tokens(None, cu, 10, out[0][:10], out[1][:10])
+    assert case.cache.error() == kvq.KVQ_DEVERR_PREFILL_LEN
+    assert not torch.any(out[0][:7] == 7.0) and torch.all(out[0][7:] == 7.0) and torch.all(out[1][7:] == 7.0)
+
+
 def test_append_chunk_bad_page():
     case = Case(4, [40, 40], [40, 40], G=16, R=16, paged=True, seed=13).fill()
     table = case.cache.region("page_table").view(torch.int32).view(2, -1)
