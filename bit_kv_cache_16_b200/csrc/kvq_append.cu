@@ -60,10 +60,11 @@ __device__ __forceinline__ void ring_put(const kvq_cache& c, const uint16_t* k, 
   *reinterpret_cast<uint4*>((uint16_t*)c.v_res + dst) = *reinterpret_cast<const uint4*>(v + src);
 }
 
-// Grid (groups + tail, H_kv, B), 128 threads.  The tokens [nq1, n1) end up in
+// Grid ((groups + tail) x H_kv, B), 128 threads; the heads are neighbours in the
+// grid, as their rows are in memory.  The tokens [nq1, n1) end up in
 // the window, the whole groups of [nq, nq1) are quantized; a group's tokens
 // come from the ring (t < n) and from the chunk (t >= n).
-//  * blockIdx.x < groups: one group of (b, h), with the prefill's team of
+//  * item < groups: one group of (b, h), with the prefill's team of
 //    four warps.  A window slot that held one of the group's tokens is free
 //    only now: this CTA also stores the new token that takes the slot, after
 //    its last read of the group (a slot's old token is always in a group that
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(128, SPARSE ? 5 : (G <= 32 ? 6 : 5))
                             int groups) {
   grid_dependents_launch();   // the commit kernel may be scheduled; it waits for this grid
   const kvq_shape& s = c.shape;
-  const int item = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int item = blockIdx.x / s.num_kv_heads, h = blockIdx.x % s.num_kv_heads, b = blockIdx.y, tid = threadIdx.x;
   const int Ws = window_slots(s);
   const ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
   if (p.err && item == 0 && h == 0 && tid == 0) set_err(c.err_word, p.err);
@@ -167,7 +168,7 @@ __device__ __forceinline__ void fp8_token_tile(const uint16_t* rows, int64_t str
   }
 }
 
-// Grid (ceil(tiles / 2), H_kv, B), 128 threads: the 16-token tiles that the
+// Grid (ceil(tiles / 2) x H_kv, B), 128 threads: the 16-token tiles that the
 // chunk's tokens [n, n1) of an FP8 or INT8 cache fall into, two per CTA
 // (warps 0 and 1 the key rows, warps 2 and 3 the value rows).  One warp owns
 // a whole value tile, so the tokens that a partly filled first tile already
@@ -178,10 +179,11 @@ __global__ void __launch_bounds__(128, I8 ? 6 : 8)
                               const int32_t* __restrict__ cu, int total, int max_new) {
   grid_dependents_launch();
   const kvq_shape& s = c.shape;
-  const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5;
+  const int item = blockIdx.x / s.num_kv_heads, h = blockIdx.x % s.num_kv_heads, b = blockIdx.y;
+  const int warp = threadIdx.x >> 5;
   const ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
-  if (p.err && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) set_err(c.err_word, p.err);
-  const int tile = p.n / kTile + 2 * blockIdx.x + (warp & 1);
+  if (p.err && blockIdx.x == 0 && threadIdx.x == 0) set_err(c.err_word, p.err);
+  const int tile = p.n / kTile + 2 * item + (warp & 1);
   if (p.m == 0 || tile * kTile >= p.n1) return;
   const int first = max(p.n - tile * kTile, 0), valid = min(kTile, p.n1 - tile * kTile);
   const int64_t stride = (int64_t)s.num_kv_heads * kHeadDim;
@@ -230,8 +232,9 @@ cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v
   const int most = min(max_new, s.capacity);         // longer chunks are rejected on the device
   if (is_token_cache(s.format)) {
     // a chunk of m tokens touches at most (m + 30) / 16 tiles
-    dim3 grid(((most + 2 * kTile - 2) / kTile + 1) / 2, s.num_kv_heads, s.batch);
-    if (grid.x == 0) grid.x = 1;
+    const long long x = max(1, ((most + 2 * kTile - 2) / kTile + 1) / 2) * (long long)s.num_kv_heads;
+    if (x > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    dim3 grid((unsigned)x, s.batch);
     if (is_int8(s.format)) append_chunk_token_kernel<true><<<grid, 128, 0, st>>>(c, kk, vv, cu, total, max_new);
     else append_chunk_token_kernel<false><<<grid, 128, 0, st>>>(c, kk, vv, cu, total, max_new);
   } else {
@@ -239,7 +242,9 @@ cudaError_t launch_append_chunk(const kvq_cache& c, const void* k, const void* v
     // window tokens are at most m and at most R + G
     const int groups = 1 + most / s.group;
     const int tail = (min(most, window_slots(s)) + 31) / 32;
-    dim3 grid(groups + tail, s.num_kv_heads, s.batch);
+    const long long x = (long long)(groups + tail) * s.num_kv_heads;
+    if (x > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    dim3 grid((unsigned)x, s.batch);
 #define KVQ_CHUNK_CASE(B, GG, SP) \
   if (s.format == B && s.group == GG && (bool)s.sparse == SP) \
     append_chunk_int_kernel<B, GG, SP><<<grid, 128, 0, st>>>(c, kk, vv, cls, cu, total, max_new, groups);

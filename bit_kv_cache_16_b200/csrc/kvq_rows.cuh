@@ -64,14 +64,22 @@ __device__ __forceinline__ bool tile_src(const kvq_cache& c, int b, int h, int t
   return true;
 }
 
-// A code of up to 8 bits -> fp32: OR-ed into the mantissa of 2^23, exactly.
-__device__ __forceinline__ float code_f32(uint32_t code) { return __uint_as_float(0x4B000000u | code) - 8388608.f; }
-
+// Codes -> numbers, two at a time, each rounded as the scalar steps would be:
+// a code of `bits` bits at bit `pos` of w (pos + bits <= 23), OR-ed into the
+// mantissa of 2^23, is 2^23 + 2^pos code; the difference is exact, and 2^-pos is
+// taken up by the scale (a power of two: exact), so that x^ = code * s + z is
+// one fp32 fma.
+constexpr uint32_t kMagic = 0x4B000000u;     // 2^23
+__device__ __forceinline__ pair_t magic_codes(uint32_t a, uint32_t b) {
+  return pair_add(pair(__uint_as_float(a), __uint_as_float(b)), pair(-8388608.f, -8388608.f));
+}
+__device__ __forceinline__ float pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 __device__ __forceinline__ float e4m3_f32(uint32_t byte) { return __half2float(u32_as_h2(e4m3x2_to_h2(byte)).x); }
 
 // Key rows: lane owns channels [8j, 8j + 8), j = lane % 16, of the tile's rows
 // 2i + lane / 16; emit(row, channel, x[8]) for each of rows [lo, hi).
-template <int BITS, bool PER_TOKEN, class Emit>
+// SP: dense-and-sparse.
+template <int BITS, bool PER_TOKEN, bool SP, class Emit>
 __device__ __forceinline__ void key_rows_bits(const TileSrc& d, int lo, int hi, Emit emit) {
   const int lane = threadIdx.x & 31, j = lane & 15, half = lane >> 4;
   float s[8], z[8];
@@ -80,7 +88,6 @@ __device__ __forceinline__ void key_rows_bits(const TileSrc& d, int lo, int hi, 
   for (int i = 0; i < 8; ++i) {
     s[i] = d.ks;                    // FP8: code * scale
     z[i] = 0.f;
-    kept[i] = 0xFFFFFFFFu;          // no token of a group has this index
   }
   if constexpr (BITS == 4 && !PER_TOKEN) {
     // the 8 channels' pairs are stored in the order (0,2) (1,3) (4,6) (5,7)
@@ -90,7 +97,8 @@ __device__ __forceinline__ void key_rows_bits(const TileSrc& d, int lo, int hi, 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int u = (r & 1) + 4 * (r >> 1);
-      s[u] = __low2float(u32_as_h2(sw[r])); s[u + 2] = __high2float(u32_as_h2(sw[r]));
+      s[u] = __low2float(u32_as_h2(sw[r])) * pow2_neg(4 * (u & 3));
+      s[u + 2] = __high2float(u32_as_h2(sw[r])) * pow2_neg(4 * ((u + 2) & 3));
       z[u] = __low2float(u32_as_h2(zw[r])); z[u + 2] = __high2float(u32_as_h2(zw[r]));
     }
   } else if constexpr (BITS == 2 && !PER_TOKEN) {
@@ -101,11 +109,11 @@ __device__ __forceinline__ void key_rows_bits(const TileSrc& d, int lo, int hi, 
     const uint32_t sw[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, zw[8] = {e.x, e.y, e.z, e.w, f.x, f.y, f.z, f.w};
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      s[r] = (j & 1) ? __high2float(u32_as_h2(sw[r])) : __low2float(u32_as_h2(sw[r]));
+      s[r] = ((j & 1) ? __high2float(u32_as_h2(sw[r])) : __low2float(u32_as_h2(sw[r]))) * pow2_neg(2 * r);
       z[r] = (j & 1) ? __high2float(u32_as_h2(zw[r])) : __low2float(u32_as_h2(zw[r]));
     }
   }
-  if (d.ksp) {
+  if constexpr (SP) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) kept[i] = d.ksp[8 * j + i];
   }
@@ -119,24 +127,32 @@ __device__ __forceinline__ void key_rows_bits(const TileSrc& d, int lo, int hi, 
     if constexpr (BITS == 8) {
       const uint2 w2 = *reinterpret_cast<const uint2*>(row + 8 * j);
       const uint32_t w[2] = {w2.x, w2.y};
-      float st = d.ks, zt = 0.f;
       if constexpr (PER_TOKEN) {
         const uint32_t m = *reinterpret_cast<const uint32_t*>(d.km + 2 * r);
-        st = __low2float(u32_as_h2(m));
-        zt = __high2float(u32_as_h2(m));
-      }
+        const float st = __low2float(u32_as_h2(m)), zt = __high2float(u32_as_h2(m));
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t code = (w[u >> 2] >> (8 * (u & 3))) & 0xFFu;
-        x[u] = PER_TOKEN ? fmaf(code_f32(code), st, zt) : e4m3_f32(code) * st;
+        for (int u = 0; u < 8; u += 2) {
+          const uint32_t sel = 0x7440u | (u & 3), sel2 = 0x7440u | ((u & 3) + 1);
+          unpair(pair_fma(magic_codes(prmt(w[u >> 2], kMagic, sel), prmt(w[u >> 2], kMagic, sel2)), pair(st, st),
+                          pair(zt, zt)), x[u], x[u + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = e4m3_f32((w[u >> 2] >> (8 * (u & 3))) & 0xFFu) * d.ks;
       }
     } else {
-      const uint32_t w = BITS == 4 ? *reinterpret_cast<const uint32_t*>(row + 4 * j)
-                                   : (uint32_t)*reinterpret_cast<const uint16_t*>(row + 2 * j);
+      uint32_t w = BITS == 4 ? *reinterpret_cast<const uint32_t*>(row + 4 * j)
+                             : (uint32_t)*reinterpret_cast<const uint16_t*>(row + 2 * j);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = fmaf(code_f32((w >> (BITS * u)) & ((1u << BITS) - 1u)), s[u], z[u]);
+      for (int u = 0; u < 8; u += 2) {
+        if (BITS == 4 && u == 4) w >>= 16;
+        const int p = BITS == 4 ? 4 * (u & 3) : 2 * u;
+        constexpr uint32_t mask = (1u << BITS) - 1u;
+        unpair(pair_fma(magic_codes(lop_or(w, mask << p, kMagic), lop_or(w, mask << (p + BITS), kMagic)),
+                        pair(s[u], s[u + 1]), pair(z[u], z[u + 1])), x[u], x[u + 1]);
+      }
     }
-    if (d.ksp) {
+    if constexpr (SP) {
 #pragma unroll
       for (int u = 0; u < 8; ++u)
         if ((int)(kept[u] >> 16) == d.t0 + r) x[u] = bf16_lo(kept[u]);
@@ -147,17 +163,18 @@ __device__ __forceinline__ void key_rows_bits(const TileSrc& d, int lo, int hi, 
 
 template <int FMT, class Emit>
 __device__ __forceinline__ void key_rows(const TileSrc& d, int lo, int hi, Emit emit) {
-  if constexpr (FMT == 8) key_rows_bits<8, false>(d, lo, hi, emit);
-  else if constexpr (FMT == 16) key_rows_bits<8, true>(d, lo, hi, emit);
+  if constexpr (FMT == 8) key_rows_bits<8, false, false>(d, lo, hi, emit);
+  else if constexpr (FMT == 16) key_rows_bits<8, true, false>(d, lo, hi, emit);
   else if constexpr (FMT == 6) {
-    if (d.bits == 4) key_rows_bits<4, false>(d, lo, hi, emit);
-    else key_rows_bits<2, false>(d, lo, hi, emit);
-  } else key_rows_bits<FMT, false>(d, lo, hi, emit);
+    if (d.bits == 4) key_rows_bits<4, false, false>(d, lo, hi, emit);
+    else key_rows_bits<2, false, false>(d, lo, hi, emit);
+  } else if (d.ksp) key_rows_bits<FMT, false, true>(d, lo, hi, emit);
+  else key_rows_bits<FMT, false, false>(d, lo, hi, emit);
 }
 
 // Value rows: lane (n, l) owns channels [16n, 16n + 16) of tokens 2l, 2l+1,
-// 2l+8, 2l+9 (the tile's layout); emit(row, channel, x[8]) twice per token.
-template <int BITS, bool FP8, class Emit>
+// 2l+8, 2l+9 (the tile's layout); emit(row, channel, x[16]) once per token.
+template <int BITS, bool FP8, bool SP, class Emit>
 __device__ __forceinline__ void value_rows_bits(const TileSrc& d, int lo, int hi, Emit emit) {
   constexpr int NW = 2 * BITS;         // words per lane
   const int lane = threadIdx.x & 31, n = lane >> 2, l = lane & 3;
@@ -168,8 +185,12 @@ __device__ __forceinline__ void value_rows_bits(const TileSrc& d, int lo, int hi
     w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 4; ++q) {        // byte q of every word is this token's
     const int r = 2 * l + (q & 1) + 8 * (q >> 1);
+    if (BITS < 8 && q == 2) {
+#pragma unroll
+      for (int i = 0; i < NW; ++i) w[i] >>= 16;
+    }
     if (r < lo || r >= hi) continue;
     float s = d.vs, z = 0.f;
     if constexpr (!FP8) {
@@ -177,31 +198,47 @@ __device__ __forceinline__ void value_rows_bits(const TileSrc& d, int lo, int hi
       s = __low2float(u32_as_h2(m));
       z = __high2float(u32_as_h2(m));
     }
-    const uint32_t kept = d.vsp ? d.vsp[r] : 0xFFFFFFFFu;
-    constexpr int PW = 8 / BITS;       // channels per byte of a word
+    float x[16];
+    if constexpr (FP8) {
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      float x[8];
+      for (int u = 0; u < 16; ++u) x[u] = e4m3_f32((w[u] >> (8 * q)) & 0xFFu) * s;
+    } else if constexpr (BITS == 8) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int ch = 8 * hh + u;
-        const uint32_t code = (w[ch / PW] >> (8 * q + BITS * (ch % PW))) & ((1u << BITS) - 1u);
-        x[u] = FP8 ? e4m3_f32(code) * s : fmaf(code_f32(code), s, z);
-        if ((int)(kept >> 16) == 16 * n + ch) x[u] = bf16_lo(kept);
+      for (int u = 0; u < 16; u += 2)
+        unpair(pair_fma(magic_codes(prmt(w[u], kMagic, 0x7440u | q), prmt(w[u + 1], kMagic, 0x7440u | q)), pair(s, s),
+                        pair(z, z)), x[u], x[u + 1]);
+    } else {
+      constexpr int PW = 8 / BITS;     // channels per byte of a word
+      constexpr uint32_t mask = (1u << BITS) - 1u;
+#pragma unroll
+      for (int c = 0; c < PW; c += 2) {
+        const int p = 8 * (q & 1) + BITS * c;
+        const pair_t s2 = pair(s * pow2_neg(p), s * pow2_neg(p + BITS)), z2 = pair(z, z);
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+          unpair(pair_fma(magic_codes(lop_or(w[i], mask << p, kMagic), lop_or(w[i], mask << (p + BITS), kMagic)), s2, z2),
+                 x[PW * i + c], x[PW * i + c + 1]);
       }
-      emit(r, 16 * n + 8 * hh, x);
     }
+    if constexpr (SP) {
+      const uint32_t kept = d.vsp[r];
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        if ((int)(kept >> 16) == 16 * n + u) x[u] = bf16_lo(kept);
+    }
+    emit(r, 16 * n, x);
   }
 }
 
 template <int FMT, class Emit>
 __device__ __forceinline__ void value_rows(const TileSrc& d, int lo, int hi, Emit emit) {
-  if constexpr (FMT == 8) value_rows_bits<8, true>(d, lo, hi, emit);
-  else if constexpr (FMT == 16) value_rows_bits<8, false>(d, lo, hi, emit);
+  if constexpr (FMT == 8) value_rows_bits<8, true, false>(d, lo, hi, emit);
+  else if constexpr (FMT == 16) value_rows_bits<8, false, false>(d, lo, hi, emit);
   else if constexpr (FMT == 6) {
-    if (d.bits == 4) value_rows_bits<4, false>(d, lo, hi, emit);
-    else value_rows_bits<2, false>(d, lo, hi, emit);
-  } else value_rows_bits<FMT, false>(d, lo, hi, emit);
+    if (d.bits == 4) value_rows_bits<4, false, false>(d, lo, hi, emit);
+    else value_rows_bits<2, false, false>(d, lo, hi, emit);
+  } else if (d.vsp) value_rows_bits<FMT, false, true>(d, lo, hi, emit);
+  else value_rows_bits<FMT, false, false>(d, lo, hi, emit);
 }
 
 }  // namespace kvq

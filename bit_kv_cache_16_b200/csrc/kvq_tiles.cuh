@@ -521,7 +521,17 @@ __device__ __noinline__ int values_any(const TileSrc& d, int quant, const RawRow
       }
       put_value8(tile, kTile * sub + row_of_token(r), ch / 8, y);
     };
-    if (quant > 0) value_rows<FMT>(d, 0, quant, one);
+    if (quant > 0)
+      value_rows<FMT>(d, 0, quant, [&](int r, int ch, const float (&x)[16]) {
+        float a[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] = x[i];
+          b[i] = x[8 + i];
+        }
+        one(r, ch, a);
+        one(r, ch + 8, b);
+      });
     for (int r = quant + half; r < kTile; r += 2) {
       float x[8];
       unpack8(raw.load(base + r, r, p), x);

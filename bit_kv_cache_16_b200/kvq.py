@@ -112,7 +112,15 @@ def load(path: Optional[str] = None):
     return lib
 
 
+def _current_stream(index: int) -> int:
+    """Handle of the device's current stream (the handle alone: a Stream object costs 3 us)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream(stream) -> ctypes.c_void_p:
+    if type(stream) is int:
+        return ctypes.c_void_p(stream)
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
@@ -399,10 +407,12 @@ class Cache:
 
     def _call(self, fn, stream, *args):
         """fn(descriptor, *args, stream) with the cache's device current, on its current stream unless one is given."""
+        if stream is None:
+            stream = _current_stream(self._index)
         if torch.cuda.current_device() == self._index:
-            return fn(self.desc, *args, torch.cuda.current_stream() if stream is None else stream)
+            return fn(self.desc, *args, stream)
         with torch.cuda.device(self._index):
-            return fn(self.desc, *args, torch.cuda.current_stream() if stream is None else stream)
+            return fn(self.desc, *args, stream)
 
     def reset(self):
         """Empty the cache: every sequence has no token (the FP8 scales stay)."""
