@@ -17,7 +17,8 @@ struct ChunkPlan {
   uint32_t err;
 };
 
-// Every thread of the block calls this and gets the same plan.
+// Every thread of the block calls this and gets the same plan: state and row
+// checks here, the pages in check_pages.
 __device__ __forceinline__ ChunkPlan chunk_plan(const kvq_cache& c, const int32_t* cu, int b, int total, int max_new) {
   const kvq_shape& s = c.shape;
   ChunkPlan p;
@@ -33,20 +34,22 @@ __device__ __forceinline__ ChunkPlan chunk_plan(const kvq_cache& c, const int32_
   p.n1 = p.n + p.m;
   p.nq1 = is_token_cache(s.format) ? p.n1 : max(p.nq, quantized_prefix(p.n1, s.residual, s.group));
   if (p.err) p.nq1 = p.nq;
-  if (s.page_size != 0 && p.nq1 > p.nq) {
-    // one page per group: a bad page id drops the sequence's whole chunk
-    bool ok = true;
-    const int32_t* table = c.page_table + (size_t)b * s.max_pages_per_seq;
-    for (int g = p.nq / kTile + threadIdx.x; g < p.nq1 / kTile; g += blockDim.x)
-      ok = ok && table[g] >= 0 && table[g] < s.num_pages;
-    if (!__syncthreads_and(ok)) {
-      p.err = KVQ_DEVERR_PAGE_RANGE;
-      p.m = 0;
-      p.n1 = p.n;
-      p.nq1 = p.nq;
-    }
-  }
   return p;
+}
+
+// One page per group: a bad page id drops the sequence's whole chunk.
+__device__ __forceinline__ void check_pages(const kvq_cache& c, int b, ChunkPlan& p) {
+  const kvq_shape& s = c.shape;
+  if (s.page_size == 0 || p.nq1 <= p.nq) return;
+  bool ok = true;
+  const int32_t* table = c.page_table + (size_t)b * s.max_pages_per_seq;
+  for (int g = p.nq / kTile + threadIdx.x; g < p.nq1 / kTile; g += blockDim.x)
+    ok = ok && table[g] >= 0 && table[g] < s.num_pages;
+  if (__syncthreads_and(ok)) return;
+  p.err = KVQ_DEVERR_PAGE_RANGE;
+  p.m = 0;
+  p.n1 = p.n;
+  p.nq1 = p.nq;
 }
 
 // Key and value row of new token t of (b, h) into its window slot (16-byte
@@ -82,7 +85,14 @@ __global__ void __launch_bounds__(128, SPARSE ? 5 : (G <= 32 ? 6 : 5))
   const kvq_shape& s = c.shape;
   const int item = blockIdx.x / s.num_kv_heads, h = blockIdx.x % s.num_kv_heads, b = blockIdx.y, tid = threadIdx.x;
   const int Ws = window_slots(s);
-  const ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
+  ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
+  // A group of new tokens alone touches nothing that is in use yet, so it looks
+  // at its own page only (34.8 -> 30.7 us for 16 sequences of up to 1301 tokens
+  // in 16-token pages); what frees or fills window slots needs the whole chunk
+  // to be good.
+  const int gs = p.nq + item * G;
+  const bool fresh_group = item < groups && gs >= p.n && item > 0;
+  if (!fresh_group) check_pages(c, b, p);
   if (p.err && item == 0 && h == 0 && tid == 0) set_err(c.err_word, p.err);
   const int lo = max(p.n, p.nq1);                    // new window tokens: [lo, n1)
   if (item >= groups) {
@@ -93,10 +103,9 @@ __global__ void __launch_bounds__(128, SPARSE ? 5 : (G <= 32 ? 6 : 5))
     }
     return;
   }
-  const int gs = p.nq + item * G;
   if (gs >= p.nq1) return;
   GroupDst d;
-  group_dst(c, b, h, gs / G, d);                     // the pages were checked with the plan
+  if (!group_dst(c, b, h, gs / G, d)) return;        // (reported with the other pages)
   const int64_t stride = (int64_t)s.num_kv_heads * kHeadDim;
   const int held = min(max(p.n - gs, 0), G);         // tokens of the group that are in the ring
   const int64_t fresh = ((int64_t)(p.t0 + gs + held - p.n) * s.num_kv_heads + h) * kHeadDim;
@@ -210,7 +219,8 @@ __global__ void __launch_bounds__(128) append_chunk_commit_kernel(kvq_cache c, c
   grid_dependency_wait();     // every CTA of the chunk kernel has read the state
   const kvq_shape& s = c.shape;
   const int b = blockIdx.x;
-  const ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
+  ChunkPlan p = chunk_plan(c, cu, b, total, max_new);
+  check_pages(c, b, p);
   if (p.err) return;
   if (is_mixed(s.format)) {
     const int Ws = window_slots(s);

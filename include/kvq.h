@@ -409,7 +409,8 @@ kvq_status kvq_merge_partials(const float *outs, const float *lses, int32_t part
  * (KVQ_DEVERR_PREFILL_LEN),
  * does not fit the capacity (KVQ_DEVERR_APPEND_FULL), needs a page whose id is
  * out of range (KVQ_DEVERR_PAGE_RANGE) or finds an inconsistent state
- * (KVQ_DEVERR_STATE).  Two launches; the second (counters) waits for the
+ * (KVQ_DEVERR_STATE); pages that hold no counted token yet may have been
+ * written all the same.  Two launches; the second (counters) waits for the
  * first on the device.
  */
 kvq_status kvq_append_chunk(kvq_cache *cache, const void *k_new_bf16, const void *v_new_bf16,
