@@ -177,6 +177,16 @@ __device__ __forceinline__ uint32_t tm_o(uint32_t tmem, int i) { return tmem + 2
 
 // --- the kernel -----------------------------------------------------------
 
+// The scaling of subtiles of kinds 0 and 1.
+struct Scaling {
+  float kmul, vlog, vinv;
+};
+// FP8 codes stand for themselves in the tiles; the head's static scales come in here.
+__device__ __forceinline__ Scaling static_scaling(const kvq_cache& c, int kv) {
+  const float vs = fmaxf(c.fp8_scale[c.shape.num_kv_heads + kv], 0x1p-100f);
+  return Scaling{c.fp8_scale[kv], log2f(vs), 1.f / vs};
+}
+
 // A subtile that is not a whole quantized one, both tiles; its description
 // goes into `info`.  Returns its kind.  (A function of its own with few
 // arguments: its registers are not the fast path's.)
@@ -189,6 +199,7 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
   const bool rope = s.rope_theta > 0.f;
   const int lane = threadIdx.x & 31;
   const int quant = min(max(sq.nq - base, 0), kTile);        // quantized rows come first
+  const bool codes = FMT == 8 && quant == kTile;             // (codes as they are: the static scales come in later)
   int ek = 0, ev = 0;
   uint32_t bad = 0u;
   TileSrc d;
@@ -236,14 +247,16 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       k_done = rows_to_tile(x[0], kt, sub, true);
       v_done = rows_to_tile(x[1], vt, sub, false);
     }
+    if (codes) d.ks = d.vs = 1.f;
     if (!k_done) ek = keys_any<FMT>(d, quant, raw, base, rope ? C.freq : nullptr, kt, sub);
     if (!v_done) ev = values_any<FMT>(d, quant, raw_v, base, vt, sub, bad);
   }
-  if (ek == 0 && ev == 0 && bad == 0u) return FMT == 8 ? 1 : 0;
+  if (ek == 0 && ev == 0 && bad == 0u) return FMT == 8 && !codes ? 1 : 0;
   if (lane == 0) {
-    info.kmul[sub] = scale_by(1.f, ek);
-    info.vlog[sub] = (float)ev;
-    info.vinv[sub] = scale_by(1.f, -ev);
+    const Scaling p = codes ? static_scaling(c, C.work.kv) : Scaling{1.f, 0.f, 1.f};
+    info.kmul[sub] = scale_by(p.kmul, ek);
+    info.vlog[sub] = p.vlog + (float)ev;
+    info.vinv[sub] = scale_by(p.vinv, -ev);
     info.bad[sub] = bad;
   }
   return 2;
@@ -402,16 +415,15 @@ __device__ __forceinline__ bool issue_all(ChunkCtrl& C, uint32_t q_tiles, uint32
       const int n = i ? n1 : n0;
       if (it >= n) continue;
       const bool done = !SHARED || i == closer;
-      if (!full(C.v_full, kValueStages, i, it) || !warp_wait(&C.p_ready[i][0], it & 1, &C.abort)) return false;
+      // (what the producers owe first: it is there as a rule)
+      if (!full(C.v_full, kValueStages, i, it) || (it + 1 < n && !full(C.k_full, kStages, i, it + 1))) return false;
+      if (!warp_wait(&C.p_ready[i][0], it & 1, &C.abort)) return false;
       tc_after();
       values(i, it, 0, false, false);
       if (!warp_wait(&C.p_ready[i][1], it & 1, &C.abort)) return false;
       tc_after();
       values(i, it, 1, done, it + 1 == n);
-      if (it + 1 >= n) continue;
-      if (!full(C.k_full, kStages, i, it + 1)) return false;
-      tc_after();
-      scores(i, it + 1, done);
+      if (it + 1 < n) scores(i, it + 1, done);
     }
   return true;
 }
@@ -427,10 +439,6 @@ struct RowState {
   float m, l;                                // reference (log2 units) and sum of this thread's row
 };
 
-// The scaling of subtiles of kinds 0 and 1.
-struct Scaling {
-  float kmul, vlog, vinv;
-};
 
 // One stream's softmax state in a thread: it owns one row.
 struct Row {
@@ -681,11 +689,7 @@ __device__ __forceinline__ void soften(const ChunkAttnArgs& A, ChunkCtrl& C, int
       C.seen[4 * i + row / 32] = make_int2(
           A.window > 0 ? W.sq.n + min(w0 + 31, last) / W.gq - A.window + 1 : 0, W.sq.n + min(w0, last) / W.gq);
     __syncwarp();
-    Scaling packed{1.f, 0.f, 1.f};           // FP8 codes stand for themselves; the static scales come in here
-    if (FMT == 8) {
-      const float vs = fmaxf(A.c.fp8_scale[A.c.shape.num_kv_heads + W.kv], 0x1p-100f);
-      packed = Scaling{A.c.fp8_scale[W.kv], log2f(vs), 1.f / vs};
-    }
+    const Scaling packed = FMT == 8 ? static_scaling(A.c, W.kv) : Scaling{1.f, 0.f, 1.f};
     for (int it = 0; it < tiles; ++it) {
       const int g = SHARED ? it : 2 * it + i, slot = g % kInfos;
       const int t0 = W.range.tile(W.first + g) * kKeys;

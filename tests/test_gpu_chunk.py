@@ -596,3 +596,163 @@ def test_hidden_values_do_not_reach_the_row():
         got = decode_window(case, 20, 3)
         for a, b in zip(clean, got):
             assert np.array_equal(a, b), fmt
+
+
+# ---------------------------------------------------------------------------
+# Ranges, scales and use
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 1e-6, 3.0])
+def test_softmax_scales(scale):
+    """Any finite softmax scale: 0 (the plain mean), negative, tiny, and one that leaves little but the largest score."""
+    case = Case(4, [200, 0], [40, 3], seed=120).fill()
+    c = case.cache
+    out = torch.empty(43, 8, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(c.chunk_workspace_bytes(2, 43, 40, 200), 16), dtype=torch.uint8, device="cuda")
+    c.chunk_attention(to_dev(case.q), to_dev(case.kn), to_dev(case.vn), case.cu_new, 40, out, scale, ws, 2, 200)
+    o2 = torch.empty(2, 8, 128, device="cuda")
+    ws = torch.empty(c.window_workspace_bytes(0, 200, 90, 2), dtype=torch.uint8, device="cuda")
+    c.decode_attention_window(to_dev(case.w.q), o2, scale, 90, 2, ws, 0, 200)
+    torch.cuda.synchronize()
+    st, at = GpuState(c), 0
+    for b, (n, m) in enumerate(zip(case.lens, case.new)):
+        for h in range(8):
+            k, v = cached_rows(st, b, h // 4)
+            if n:
+                ref, _, tol = attend(bf16(case.w.q[b, h])[None], k, v, [n - 1], scale, 90, 2, rounded=False)
+                assert np.all(np.abs(o2[b, h].cpu().numpy() - ref[0]) <= tol[0])
+            k = np.concatenate([k, bf16(case.kn[at:at + m, h // 4])])
+            v = np.concatenate([v, bf16(case.vn[at:at + m, h // 4])])
+            ref, _, tol = attend(bf16(case.q[at:at + m, h]), k, v, np.arange(n, n + m), scale)
+            assert np.all(np.abs(out[at:at + m, h].float().cpu().numpy() - ref) <= tol), (b, h)
+        at += m
+
+
+@pytest.mark.parametrize("n,kexp,vexp,qexp", [(70, 17, 0, -17), (0, -20, 20, 20), (70, 0, -30, 0), (70, 0, 60, 0),
+                                              (70, 30, -60, -30), (0, -60, -60, 60)])
+def test_chunk_of_any_magnitude(n, kexp, vexp, qexp):
+    """New tokens (and queries) far outside fp16's range beside cached ones of ordinary size: the powers of two taken out
+    of their rows come back in the scores and the output."""
+    case = Case(4, [n], [40], R=64, seed=121).fill()
+    up = lambda a, e: bits_of(bf16(a) * 2.0 ** e)
+    case.kn, case.vn, case.q = up(case.kn, kexp), up(case.vn, vexp), up(case.q, qexp)
+    case.check(case.attend())
+    assert case.cache.error() == 0
+    # the same tokens from the window ring
+    case.append(case.kn, case.vn, None, [40])
+    case.lens, case.kn, case.vn, case.q = [n + 40], case.kn[:5], case.vn[:5], case.q[:5]
+    case.new, case.cu_new = [5], cu_of([5])
+    assert GpuState(case.cache).n_quant[0] <= n               # none of the new tokens is quantized
+    case.check(case.attend())
+
+
+@pytest.mark.parametrize("fmt", [4, 8, 16, 2])
+def test_chunk_hidden_cached_values(fmt):
+    """NaN and infinities in cached tokens that the window hides from every row change nothing."""
+    case = Case(fmt, [330], [20], R=0, seed=122).fill()
+    clean = case.attend(window=60, sinks=3)
+    kq, vq = case.k.copy(), case.v.copy()
+    for t, x in ((100, 0x7FC0), (150, 0x7F80), (200, 0x7FC0)):
+        kq[t], vq[t] = x, x
+    vq[[10, 262, 268]] = np.array([0x7FC0, 0x7F80, 0x7FC0])[:, None, None]      # beside visible ones (values: by token)
+    case.cache.reset()
+    case.append(kq, vq, None, [330])
+    got = case.attend(window=60, sinks=3)
+    # rows 0 .. : the first visible token of row 0 is 330 - 59 = 271
+    assert np.array_equal(got, clean)
+
+
+def test_chunk_visible_nan_makes_its_rows_nan():
+    case = Case(16, [100], [30], seed=123).fill()
+    vq = case.v.copy()
+    vq[60, 1] = 0x7FC0
+    case.cache.reset()
+    case.append(case.k, vq, None, [100])
+    out = case.attend(window=60, sinks=0)
+    # row i sees tokens > 100 + i - 60: token 60 for i < 20
+    assert not np.any(np.isfinite(out[:20, 4:])) and np.all(np.isfinite(out[20:])) and np.all(np.isfinite(out[:, :4]))
+
+
+def test_calls_on_two_streams():
+    """Two caches attended and appended on two streams at once give what they give one after the other."""
+    cases = [Case(f, [900, 33], [70, 5], seed=124 + f).fill() for f in (4, 16)]
+    want = [c.attend(splits=2) for c in cases]
+    args = []
+    for c in cases:
+        n = c.cache.chunk_workspace_bytes(2, 75, 70, 900)
+        args.append([to_dev(c.q), to_dev(c.kn), to_dev(c.vn), torch.empty(75, 8, 128, dtype=torch.bfloat16, device="cuda"),
+                     torch.empty(n, dtype=torch.uint8, device="cuda")])
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, (q, k, v, out, ws) in zip(cases, streams, args):
+            c.cache.chunk_attention(q, k, v, c.cu_new, 70, out, SCALE, ws, 2, 900, stream=s)
+    torch.cuda.synchronize()
+    for c, w, a in zip(cases, want, args):
+        assert np.array_equal(a[3].float().cpu().numpy().astype(np.float64), w)
+
+
+def test_window_decode_captured():
+    """Append, windowed decode and read back in a graph, replayed while the sequences grow."""
+    case = Case(2, [300, 7], [1, 1], G=16, R=16, seed=126, extra=8).fill()
+    c = case.cache
+    k, v = to_dev(case.kn), to_dev(case.vn)
+    q, out, lse = to_dev(case.w.q), torch.empty(2, 8, 128, device="cuda"), torch.empty(2, 8, device="cuda")
+    ws = torch.empty(c.window_workspace_bytes(0, 320, 100, 4), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        c.append_chunk(k, v, case.cu_new, 1)
+        c.decode_attention_window(q, out, SCALE, 100, 4, ws, 0, 320, lse=lse)
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        case.lens = [300 + 2 + i, 7 + 2 + i]
+        check_decode(case, (out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)), 100, 4)
+    assert c.error() == 0
+
+
+def test_long_offsets():
+    """A unit whose packed rows pass 2^31 bytes: reads, chunk attention and windowed decode at its far end."""
+    cap = 17 * 2 ** 20                                       # x 128 bytes per row = 2.1 GiB of keys for one head
+    c = kvq.Cache(16, 1, 2, 1, cap)
+    n = cap - 300
+    c.seq_len()[0] = c.n_quant()[0] = n
+    rng = np.random.default_rng(7)
+    k, v = (to_dev(bits_of(rng.standard_normal((200, 1, 128)))) for _ in range(2))
+    cu = cu_of([200])
+    c.append_chunk(k, v, cu, 200)
+    out = [torch.empty(200, 1, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    c.read_tokens(torch.tensor([n], dtype=torch.int32, device="cuda"), cu, 200, *out)
+    q, kn, vn = (to_dev(bits_of(rng.standard_normal((7, h, 128)))) for h in (2, 1, 1))
+    o = torch.empty(7, 2, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(c.chunk_workspace_bytes(3, 7, 7, cap, 150), 16), dtype=torch.uint8, device="cuda")
+    c.chunk_attention(q, kn, vn, cu_of([7]), 7, o, SCALE, ws, 3, cap, window=150)
+    o1 = torch.empty(1, 2, 128, device="cuda")
+    ws = torch.empty(c.window_workspace_bytes(0, cap, 150), dtype=torch.uint8, device="cuda")
+    c.decode_attention_window(q[:1], o1, SCALE, 150, 0, ws, 0, cap)
+    torch.cuda.synchronize()
+    assert c.error() == 0 and c.seq_len()[0] == n + 200
+    rows = [x.float().cpu().numpy().astype(np.float64)[:, 0] for x in out]
+    for x, given in zip(rows, (k, v)):
+        g = bf16(given.cpu().numpy().view(np.uint16))[:, 0]
+        step = (g.max(1) - g.min(1))[:, None] / 255           # half a code's step and the roundings of scale, zero, bf16
+        assert np.all(np.abs(x - g) <= 0.5 * step * (1 + 2.0 ** -9) + 255 * step * 2.0 ** -11 + np.abs(g) * 2.0 ** -7)
+    # attention over what the cache holds: rows as read back are rounded to bf16, hence the wider tolerance
+    kk, vv = (np.concatenate([a, bf16(b.cpu().numpy().view(np.uint16))[:, 0]]) for a, b in zip(rows, (kn, vn)))
+    qq = bf16(q.cpu().numpy().view(np.uint16))
+    for h in range(2):
+        ref, _, tol = attend(qq[:, h], kk, vv, np.arange(200, 207), SCALE, 150)
+        d = SCALE * (np.abs(qq[:, h]) @ np.abs(kk).T).max(1)[:, None] * HALF_BF16
+        wide = tol + np.expm1(2 * d) * np.abs(vv).max() + HALF_BF16 * np.abs(vv).max()
+        assert np.all(np.abs(o[:, h].float().cpu().numpy() - ref) <= wide)
+        ref, _, _ = attend(qq[:1, h], kk[:200], vv[:200], [199], SCALE, 150)
+        assert np.all(np.abs(o1[0, h].cpu().numpy() - ref[0]) <= wide[0])
