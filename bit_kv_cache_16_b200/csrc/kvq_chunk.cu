@@ -578,17 +578,15 @@ __device__ __forceinline__ bool soft_any(const ChunkAttnArgs& A, ChunkCtrl& C, i
     return kind == 0 ? packed : kind == 1 ? Scaling{1.f, 0.f, 1.f} : Scaling{info.kmul[sub], info.vlog[sub], info.vinv[sub]};
   };
   auto bad_bits = [&](int sub) { return info.kind[sub] == 2 ? info.bad[sub] : 0u; };
-  auto scores = [&](int sub, float (&x)[16]) {
+  // scores (log2 units, with the value scale) less `ref`: the same steps as soft_plain's
+  auto scores = [&](int sub, float ref, float (&x)[16]) {
     tc_ld16(x, w.ts + kTile * sub);
     tc_wait_ld();
     const Scaling sc = scaling(sub);
-    const float k = w.cm * sc.kmul, vlog = sc.vlog;
-    const bool none = bad_bits(sub) >> 16;
+    const float k = w.cm * sc.kmul, off = sc.vlog - ref;
+    const uint32_t seen = bad_bits(sub) >> 16 ? 0u : visible64(t0 + kTile * sub, p_row, A.window, A.sinks).x;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const int t = t0 + kTile * sub + row_of_token(c);        // the order is its own inverse
-      x[c] = !none && key_visible(t, p_row, A.window, A.sinks) ? fmaf(x[c], k, vlog) : -INFINITY;
-    }
+    for (int c = 0; c < 16; ++c) x[c] = seen >> c & 1u ? fmaf(x[c], k, off) : -INFINITY;
   };
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
@@ -597,7 +595,7 @@ __device__ __forceinline__ bool soft_any(const ChunkAttnArgs& A, ChunkCtrl& C, i
 #pragma unroll 1
     for (int j = 0; j < kSubs / 2; ++j) {
       float x[16];
-      scores(s0 + j, x);
+      scores(s0 + j, 0.f, x);
 #pragma unroll
       for (int c = 0; c < 16; ++c) top = fmaxf(top, x[c]);
     }
@@ -606,13 +604,13 @@ __device__ __forceinline__ bool soft_any(const ChunkAttnArgs& A, ChunkCtrl& C, i
 #pragma unroll 1
     for (int j = 0; j < kSubs / 2; ++j) {                      // P lies over scores that have been read
       float x[16], sum = 0.f;
-      scores(s0 + j, x);
+      scores(s0 + j, ref, x);
       const uint32_t bad = bad_bits(s0 + j);
       uint32_t p[8];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         if ((bad >> c & 1u) && x[c] != -INFINITY) sum = __int_as_float(0x7FC00000);   // the row sees such a value
-        x[c] = ex2(x[c] - ref);
+        x[c] = ex2(x[c]);
         sum += x[c];
       }
 #pragma unroll
@@ -877,6 +875,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     const int busy = SHARED ? 4 : (block_rows + 31) / 32;    // softmax warps per stream
     const int pw = warp >= kProducerWarp ? warp - kProducerWarp
                                          : kProducers + (warp >> 2) * (4 - busy) + (warp & 3) - busy;
+    // (with at most two tiles' subtiles between its own, a producer leaves out no
+    // use of a stage that a barrier's parity could take for the next)
+    static_assert(kProducers + 2 * 3 <= 2 * kSubs, "producers");
     produce<FMT, SHARED>(A, C, unit, k_tiles, v_tiles, pw, kProducers + 2 * (4 - busy));
   }
   __syncthreads();

@@ -59,9 +59,4 @@ struct TileRange {
   __device__ __forceinline__ int tile(int i) const { return i < lead ? i : skip + i - lead; }
 };
 
-// Key t is visible to the row at position p.
-__device__ __forceinline__ bool key_visible(int t, int p, int window, int sinks) {
-  return t <= p && (window <= 0 || t > p - window || t < sinks);
-}
-
 }  // namespace kvq

@@ -658,8 +658,10 @@ def test_chunk_hidden_cached_values(fmt):
     case.cache.reset()
     case.append(kq, vq, None, [330])
     got = case.attend(window=60, sinks=3)
-    # rows 0 .. : the first visible token of row 0 is 330 - 59 = 271
-    assert np.array_equal(got, clean)
+    # (the first visible token of row 0 is 330 - 59 = 271.)  The weights are the same bit for bit; where a tile is looked
+    # at closely, their sum is taken in another order: 64 steps of 2^-24, which can only turn the last rounding to bf16
+    # over, by one step of at most 2^-7 of the value
+    assert np.all(np.abs(got - clean) <= 2.0 ** -7 * np.abs(clean))
 
 
 def test_chunk_visible_nan_makes_its_rows_nan():
