@@ -31,6 +31,22 @@ constexpr int kInfos = 4;                    // tile descriptions in flight
 constexpr float kSlack = 14.f;               // the reference maximum may lag by 2^14 (P stays below fp16's 65504)
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
+// Eight channels of a query row (16 lanes a row) whose magnitudes need a power
+// of two taken out, or that is not finite throughout; returns the power.
+__device__ __noinline__ float put_scaled8(uint32_t at, uint4 v) {
+  float x[8], amax = 0.f;
+  unpack8(v, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[i]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const int e = tile_exponent(amax);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = scale_by(x[i], -e);
+  st_shared16(at, pack_h2(x[0], x[4]), pack_h2(x[1], x[5]), pack_h2(x[2], x[6]), pack_h2(x[3], x[7]));
+  return scale_by(1.f, e);
+}
+
 // What every thread of a CTA knows about its work.
 struct Work {
   ChunkSeq sq;
@@ -199,7 +215,7 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
   const bool rope = s.rope_theta > 0.f;
   const int lane = threadIdx.x & 31;
   const int quant = min(max(sq.nq - base, 0), kTile);        // quantized rows come first
-  const bool codes = FMT == 8 && quant == kTile;             // (codes as they are: the static scales come in later)
+  const bool codes = FMT == 8 && quant > 0;                  // (codes as they are: the static scales come in later)
   int ek = 0, ev = 0;
   uint32_t bad = 0u;
   TileSrc d;
@@ -209,23 +225,6 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
     zero_rows(vt, sub);
     bad = 1u << 16;
   } else {
-    if (quant == kTile && !rope && !s.sparse) {              // (a tile at the window's edge)
-      SubSrc p;
-      SubWords<FMT> w;
-      sub_src<FMT>(unit, base / kTile, p);
-      load_keys<FMT>(p, w);
-      load_values<FMT>(p, w);
-      if (!values_odd<FMT>(w)) {
-        if (FMT == 6 && p.two) {
-          keys_to_tile<FMT, 2>(w, kt, sub);
-          values_to_tile<FMT, 2>(w, vt, sub);
-        } else {
-          keys_to_tile<FMT, SubWords<FMT>::kBits>(w, kt, sub);
-          values_to_tile<FMT, SubWords<FMT>::kBits>(w, vt, sub);
-        }
-        return 0;
-      }
-    }
     const size_t ring = is_token_cache(FMT) ? 0 : Addr::ring_row(s, C.work.b, C.work.kv, 0);
     const size_t at = ((size_t)sq.t0 * s.num_kv_heads + C.work.kv) * kHeadDim;
     RawRows raw;
@@ -239,6 +238,55 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
     raw.fresh = A.k + at;
     raw_v.ring = (const uint16_t*)c.v_res + ring;
     raw_v.fresh = A.v + at;
+    if (quant > 0 && !rope && !s.sparse) {
+      // packed words: a tile at the window's edge, or (8-bit formats) the
+      // sequence's last one with the chunk's first tokens behind it
+      SubSrc p;
+      SubWords<FMT> w;
+      sub_src<FMT>(unit, base / kTile, p);
+      load_keys<FMT>(p, w);
+      load_values<FMT>(p, w);
+      if (quant < kTile) drop_values<FMT>(w, quant);         // (what lies behind the end is not data)
+      // raw rows take the codes' scaling (FP8), so that the subtile has one
+      const float k_inv = codes ? 1.f / d.ks : 1.f, v_inv = codes ? 1.f / d.vs : 1.f;
+      bool fits = !values_odd<FMT>(w);
+      float amax_k = 0.f, amax_v = 0.f;
+      for (int r = quant + (lane >> 4); r < kTile; r += 2) {
+        float x[8], y[8];
+        unpack8(raw.load(base + r, r, lane & 15), x);
+        unpack8(raw_v.load(base + r, r, lane & 15), y);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          amax_k = fmaxf(amax_k, fabsf(x[u] * k_inv));
+          amax_v = fmaxf(amax_v, fabsf(y[u] * v_inv));
+          fits = fits && fabsf(x[u]) < INFINITY && fabsf(y[u]) < INFINITY;
+        }
+      }
+      fits = fits && tile_exponent(warp_max(amax_k)) == 0 && tile_exponent(warp_max(amax_v)) == 0;
+      if (__all_sync(0xffffffffu, fits)) {
+        if (FMT == 6 && p.two) {
+          keys_to_tile<FMT, 2>(w, kt, sub);
+          values_to_tile<FMT, 2>(w, vt, sub);
+        } else {
+          keys_to_tile<FMT, SubWords<FMT>::kBits>(w, kt, sub);
+          values_to_tile<FMT, SubWords<FMT>::kBits>(w, vt, sub);
+        }
+        __syncwarp();
+        for (int r = quant + (lane >> 4); r < kTile; r += 2) {
+          float x[8], y[8];
+          unpack8(raw.load(base + r, r, lane & 15), x);
+          unpack8(raw_v.load(base + r, r, lane & 15), y);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            x[u] *= k_inv;
+            y[u] *= v_inv;
+          }
+          put_key8(kt, kTile * sub + row_of_token(r), lane & 15, x);
+          put_value8(vt, kTile * sub + row_of_token(r), lane & 15, y);
+        }
+        return 0;
+      }
+    }
     bool k_done = false, v_done = false;
     if (quant == 0 && !rope) {
       RawWords x[2];                                         // both on their way at once
@@ -247,13 +295,14 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       k_done = rows_to_tile(x[0], kt, sub, true);
       v_done = rows_to_tile(x[1], vt, sub, false);
     }
-    if (codes) d.ks = d.vs = 1.f;
+    if (codes && quant == kTile) d.ks = d.vs = 1.f;          // (with raw rows: in natural scale, kind 1)
     if (!k_done) ek = keys_any<FMT>(d, quant, raw, base, rope ? C.freq : nullptr, kt, sub);
     if (!v_done) ev = values_any<FMT>(d, quant, raw_v, base, vt, sub, bad);
   }
-  if (ek == 0 && ev == 0 && bad == 0u) return FMT == 8 && !codes ? 1 : 0;
+  const bool scaled = codes && quant == kTile;
+  if (ek == 0 && ev == 0 && bad == 0u) return FMT == 8 && !scaled ? 1 : 0;
   if (lane == 0) {
-    const Scaling p = codes ? static_scaling(c, C.work.kv) : Scaling{1.f, 0.f, 1.f};
+    const Scaling p = scaled ? static_scaling(c, C.work.kv) : Scaling{1.f, 0.f, 1.f};
     info.kmul[sub] = scale_by(p.kmul, ek);
     info.vlog[sub] = p.vlog + (float)ev;
     info.vinv[sub] = scale_by(p.vinv, -ev);
@@ -839,24 +888,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
             A.q + ((size_t)(W.sq.t0 + R / W.gq) * s.num_q_heads + W.kv * W.gq + R % W.gq) * kHeadDim + 8 * p);
     }
     const uint32_t sign = A.scale_log2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll 1
+#pragma unroll 2
     for (int u = 0; u < kPer; ++u) {
       const int row = (tid >> 4) + u * (kChunkThreads / 16);
-      float x[8], amax = 0.f;
       uint4 v = w[0];
 #pragma unroll
       for (int i = 0; i + 1 < kPer; ++i) w[i] = w[i + 1];
       v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
-      unpack8(v, x);
+      uint32_t m = larger_half(abs_max8(0u, v));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[i]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int e = tile_exponent(amax);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = e ? scale_by(x[i], -e) : x[i];
-      put_key8(q_tiles + (row / kRows) * kTileBytes16, row % kRows, p, x);
-      if (p == 0) C.qmul[row] = scale_by(1.f, e);
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t at = piece_at(q_tiles + (row / kRows) * kTileBytes16, row % kRows, p);
+      float factor = 1.f;
+      if (__all_sync(0xffffffffu, ordinary(m))) {
+        put_raw8(at, v, true);
+      } else {
+        factor = put_scaled8(at, v);
+      }
+      if (p == 0) C.qmul[row] = factor;
     }
     fence_async();
   }

@@ -393,6 +393,9 @@ __device__ __forceinline__ uint32_t abs_max8(uint32_t m, const uint4& w) {
 }
 __device__ __forceinline__ uint32_t larger_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
 
+// A largest bf16 magnitude that fp16 takes as it is: 0, or in [2^-6, 2^15).
+__device__ __forceinline__ bool ordinary(uint32_t m) { return m == 0u || (m >= 0x3C80u && m < 0x4700u); }
+
 // Eight bf16 numbers -> four fp16 pairs, in the key tiles' channel order or in order.
 __device__ __forceinline__ void put_raw8(uint32_t at, const uint4& w, bool key) {
   const float x0 = bf16_lo(w.x), x1 = bf16_hi(w.x), x2 = bf16_lo(w.y), x3 = bf16_hi(w.y);
@@ -418,11 +421,28 @@ __device__ __forceinline__ bool rows_to_tile(const RawWords& x, uint32_t tile, i
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = abs_max8(m, x.w[i]);
   m = __reduce_max_sync(0xffffffffu, larger_half(m));
-  if (m != 0u && (m < 0x3C80u || m >= 0x4700u)) return false;      // outside [2^-6, 2^15)
+  if (!ordinary(m)) return false;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     put_raw8(piece_at(tile, kTile * sub + 4 * (i >> 1) + 2 * half + (i & 1), p), x.w[i], key);
   return true;
+}
+
+// Values of the subtile's tokens from `quant` on -> zero.
+template <int FMT>
+__device__ __forceinline__ void drop_values(SubWords<FMT>& w, int quant) {
+  const int l = threadIdx.x & 3;
+  uint32_t keep = 0u;                            // byte q of every 8-bit word is token 2l + q % 2 + 8 (q / 2)
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const bool in = 2 * l + (q & 1) + 8 * (q >> 1) < quant;
+    if (in) keep |= 0xFFu << (8 * q);
+    if constexpr (FMT != 8)
+      if (!in) w.vm[q] = 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < SubWords<FMT>::kVW; ++i)
+    if (SubWords<FMT>::kBits == 8) w.v[i] &= keep;
 }
 
 // Whether a value of the subtile could be anything but a finite half (its
