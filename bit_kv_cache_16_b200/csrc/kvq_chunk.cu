@@ -5,10 +5,25 @@
 // one matrix (row R = head R % gq of token R / gq).  For each tile of 128
 // tokens: S = Q K^T (128 rows x 128 keys, fp16 operands, fp32 in TMEM), the
 // online softmax with one thread per row (64 keys at a time), P = fp16 back
-// into TMEM, O += P V with O in TMEM.  Packed tokens become fp16 operands once per CTA and tile
-// (kvq_tiles.cuh); fp16 holds every code exactly and a dequantized number to
-// 2^-11, eight times finer than bf16, and powers of two are taken out of raw
-// rows that would not fit.
+// into TMEM, O += P V with O in TMEM.  Packed tokens become fp16 operands once
+// per CTA and tile (kvq_tiles.cuh); fp16 holds every code exactly and a
+// dequantized number to 2^-11, eight times finer than bf16, and powers of two
+// are taken out of raw rows that would not fit.
+//
+// What bounds it: a stream's tile is a chain (scores, maximum, weights, P V,
+// next scores) of about 2400 cycles of softmax and 1500 of products, and TMEM
+// has room for two streams (S or P and O: 256 columns each).  Together a tile
+// of 256 rows takes about 4400 cycles, of which the tensor pipe is busy 45 %,
+// the exponential unit 45 %, the issue slots 48 %.  Measured alone with a cold
+// L2: 2048 tokens over 32768 INT4 tokens, 32 / 8 heads, 1275 us (889 TFLOP/s);
+// 1000 over 65536 INT2 tokens, 64 / 8 heads, 2108 us (1026); 2 x 1024 in a
+// window of 4096 + 4 over FP8, 487 us (565); 6 tokens over 8 x 8192 INT4, 63 us
+// (1.2 TB/s of packed tokens: the paired form's chain of 33 tiles a CTA).
+//
+// Sixteen warps, because a seventeenth would leave 96 registers a thread, and
+// a spilled register is a trip to L2 here (shared memory takes the whole L1):
+// 2205 us with spills in the softmax, 1648 without.  Two softmax warpgroups
+// per stream (24 warps, 80 registers) took 1446 us against 1290.
 #include "kvq_tiles.cuh"
 
 namespace kvq {
@@ -407,7 +422,7 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, co
 // the second P V, whose P they overwrite (the tensor core takes one thread's
 // products in order), while the other stream's softmax runs.  (Scores in two
 // blocks of 64 keys, each with its own next product, were slower: a product
-// of N = 64 takes 58 cycles, one of N = 128 about 64, both bound by the query
+// of N = 64 takes 58 cycles, one of N = 128 about 72, both bound by the query
 // operand's way from shared memory.)  False: a wait was given up.
 constexpr uint32_t kStageStep = kTileBytes16 >> 4;
 
@@ -983,7 +998,8 @@ size_t chunk_workspace_bytes(const kvq_shape& s, int num_splits, int rows) {
 
 // Key ranges per row block: the fewest rounds of CTAs over the SMs, counting
 // what a CTA costs beside its tiles (set-up and output, worth about four
-// tiles).
+// tiles).  2048 tokens over 32768 (256 row blocks): 1 range 1313 us, 4 1279;
+// 6 tokens over 8 x 8192: 1 range 101 us, 2 ranges 69.
 int chunk_default_splits(const kvq_shape& s, int rows, int max_new, int max_len, int window, int sinks) {
   const long long span = window > 0 ? min((long long)max_len + max_new, (long long)window + sinks + max_new)
                                     : (long long)max_len + max_new;

@@ -1,4 +1,4 @@
-// Shared pieces of the chunk attention kernels (kvq_chunk.cu, kvq_chunk_mma.cu).
+// What the chunk attention kernels (kvq_chunk.cu) and its host code share.
 #pragma once
 
 #include "kvq_common.cuh"
