@@ -17,8 +17,9 @@
 // the exponential unit 45 %, the issue slots 48 %.  Measured alone with a cold
 // L2: 2048 tokens over 32768 INT4 tokens, 32 / 8 heads, 1275 us (889 TFLOP/s);
 // 1000 over 65536 INT2 tokens, 64 / 8 heads, 2108 us (1026); 2 x 1024 in a
-// window of 4096 + 4 over FP8, 487 us (565); 6 tokens over 8 x 8192 INT4, 63 us
-// (1.2 TB/s of packed tokens: the paired form's chain of 33 tiles a CTA).
+// window of 4096 + 4 over FP8, 525 us (524; 480 with a warm L2); 6 tokens over
+// 8 x 8192 INT4, 68 us (1.2 TB/s of packed tokens: the paired form's chain of 33
+// tiles a CTA).
 //
 // Sixteen warps, because a seventeenth would leave 96 registers a thread, and
 // a spilled register is a trip to L2 here (shared memory takes the whole L1):

@@ -67,12 +67,20 @@ __global__ void __launch_bounds__(128, 16) read_tokens_kernel(ReadArgs A) {
           make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
     });
   } else {
+    // a whole sector per store where the caller's rows start on one
+    const bool sectors = ((uintptr_t)rows & 31u) == 0;
     value_rows<FMT>(d, lo, hi, [&](int r, int ch, const float (&x)[16]) {
-      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(out + r * stride + ch),
-                   "r"(pack_bf2(x[0], x[1])), "r"(pack_bf2(x[2], x[3])), "r"(pack_bf2(x[4], x[5])),
-                   "r"(pack_bf2(x[6], x[7])), "r"(pack_bf2(x[8], x[9])), "r"(pack_bf2(x[10], x[11])),
-                   "r"(pack_bf2(x[12], x[13])), "r"(pack_bf2(x[14], x[15]))
-                   : "memory");
+      const uint4 a = make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+      const uint4 e = make_uint4(pack_bf2(x[8], x[9]), pack_bf2(x[10], x[11]), pack_bf2(x[12], x[13]), pack_bf2(x[14], x[15]));
+      uint16_t* to = out + r * stride + ch;
+      if (sectors) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z),
+                     "r"(a.w), "r"(e.x), "r"(e.y), "r"(e.z), "r"(e.w)
+                     : "memory");
+      } else {
+        *reinterpret_cast<uint4*>(to) = a;
+        *reinterpret_cast<uint4*>(to + 8) = e;
+      }
     });
   }
 }

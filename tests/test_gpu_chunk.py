@@ -305,6 +305,37 @@ def test_read_tokens_sparse_and_rope(fmt, G):
                     assert np.all(np.abs(x - ref) <= np.abs(ref) * (HALF_BF16 + 2.0 ** -20) + 1e-38)
 
 
+@pytest.mark.parametrize("fmt,G,R,paged", FORMATS)
+def test_rows_at_odd_sixteenths(fmt, G, R, paged):
+    """Arrays that start 16 bytes past a 32-byte boundary: the same numbers."""
+    case = Case(fmt, [130, 33], [40, 1], G=G, R=R, paged=paged, seed=33).fill()
+
+    def shifted(like):
+        t = torch.zeros(like.numel() + 8, dtype=like.dtype, device="cuda")[8:].view(like.shape)
+        assert t.data_ptr() % 32 == 16
+        return t.copy_(like)
+
+    rows = [torch.zeros(163, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    odd = [shifted(r) for r in rows]
+    case.cache.read_tokens(None, case.cu, 130, *rows)
+    case.cache.read_tokens(None, case.cu, 130, *odd)
+    assert torch.equal(rows[0], odd[0]) and torch.equal(rows[1], odd[1]) and rows[1].abs().sum() > 0
+    q, kn, vn = (to_dev(x) for x in (case.q, case.kn, case.vn))
+    out = [torch.zeros(41, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    out[1] = shifted(out[0])
+    case.cache.chunk_attention(q, kn, vn, case.cu_new, 40, out[0], SCALE, None, 1, 130)
+    case.cache.chunk_attention(shifted(q), shifted(kn), shifted(vn), case.cu_new, 40, out[1], SCALE, None, 1, 130)
+    assert torch.equal(*out) and out[0].abs().sum() > 0
+    other = Case(fmt, [130, 33], [40, 1], G=G, R=R, paged=paged, seed=33).fill()
+    cls = to_dev(case.clsn) if fmt == 6 else None
+    case.cache.append_chunk(kn, vn, case.cu_new, 40, token_class=cls)
+    other.cache.append_chunk(shifted(kn), shifted(vn), case.cu_new, 40, token_class=cls)
+    for name in ("k_codes", "v_codes", "k_meta", "v_meta", "k_res", "v_res", "seq_len"):
+        x, y = case.cache.buffers[name], other.cache.buffers[name]
+        assert x is None or torch.equal(x, y), name
+    assert case.cache.error() == 0 and other.cache.error() == 0
+
+
 def test_read_tokens_refused_ranges():
     case = Case(4, [50, 60, 70], [0, 0, 0], G=16, R=16, paged=True, seed=31).fill()
     out = [torch.full((100, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
