@@ -265,7 +265,7 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       if (quant < kTile) drop_values<FMT>(w, quant);         // (what lies behind the end is not data)
       // raw rows take the codes' scaling (FP8), so that the subtile has one
       const float k_inv = codes ? 1.f / d.ks : 1.f, v_inv = codes ? 1.f / d.vs : 1.f;
-      bool fits = !values_odd<FMT>(w);
+      bool fits = !values_odd<FMT>(w) && k_inv < INFINITY && v_inv < INFINITY;
       float amax_k = 0.f, amax_v = 0.f;
       for (int r = quant + (lane >> 4); r < kTile; r += 2) {
         float x[8], y[8];
@@ -1027,9 +1027,9 @@ static cudaError_t launch_form(const ChunkAttnArgs& A, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<FMT, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmem);
   if (e != cudaSuccess) return e;
-  const long long x = row_blocks(s, min(A.max_new, A.rows)) * A.splits;
+  const long long x = max(row_blocks(s, min(A.max_new, A.rows)), 1ll) * A.splits;   // (the kernel divides by the splits)
   if (x > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  dim3 grid((unsigned)max(x, 1ll), s.num_kv_heads, s.batch);
+  dim3 grid((unsigned)x, s.num_kv_heads, s.batch);
   chunk_attention_kernel<FMT, SHARED><<<grid, kChunkThreads, kSmem, st>>>(A);
   return cudaGetLastError();
 }
@@ -1053,7 +1053,7 @@ cudaError_t launch_chunk_attention(const ChunkAttnArgs& args, cudaStream_t st) {
   if (e != cudaSuccess || A.splits == 1) return e;
   const long long per_seq = (long long)min(A.max_new, A.rows) * s.num_q_heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((per_seq + 7) / 8), s.batch);
+  cfg.gridDim = dim3((unsigned)max((per_seq + 7) / 8, 1ll), s.batch);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

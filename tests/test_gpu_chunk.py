@@ -404,6 +404,18 @@ def test_chunk_attention_rope(fmt):
     case.check(case.attend(window=40, sinks=3), 40, 3, rope=10000.0)
 
 
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_chunk_attention_bound_of_zero(splits):
+    """max_new = 0: empty chunks are fine, any other is refused on the device and its rows stay."""
+    case = Case(4, [70, 9], [3, 2], seed=35).fill()
+    out = torch.full((5, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(case.cache.chunk_workspace_bytes(splits, 5, 0, 70), 16), dtype=torch.uint8, device="cuda")
+    q, kn, vn = (to_dev(x) for x in (case.q, case.kn, case.vn))
+    for cu, error in ((cu_of([0, 0]), 0), (case.cu_new, kvq.KVQ_DEVERR_PREFILL_LEN)):
+        case.cache.chunk_attention(q, kn, vn, cu, 0, out, SCALE, ws, splits, 70)
+        assert case.cache.error() == error and torch.all(out == 7.0)
+
+
 def test_chunk_attention_bad_page():
     case = Case(4, [200, 90], [20, 7], G=16, R=16, paged=True, seed=82).fill()
     st = GpuState(case.cache)
