@@ -278,7 +278,9 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
           fits = fits && fabsf(x[u]) < INFINITY && fabsf(y[u]) < INFINITY;
         }
       }
-      fits = fits && tile_exponent(warp_max(amax_k)) == 0 && tile_exponent(warp_max(amax_v)) == 0;
+      amax_k = warp_max(amax_k);                             // (whole-warp shuffles: not behind a lane's own `fits`)
+      amax_v = warp_max(amax_v);
+      fits = fits && tile_exponent(amax_k) == 0 && tile_exponent(amax_v) == 0;
       if (__all_sync(0xffffffffu, fits)) {
         if (FMT == 6 && p.two) {
           keys_to_tile<FMT, 2>(w, kt, sub);
