@@ -265,7 +265,7 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       if (quant < kTile) drop_values<FMT>(w, quant);         // (what lies behind the end is not data)
       // raw rows take the codes' scaling (FP8), so that the subtile has one
       const float k_inv = codes ? 1.f / d.ks : 1.f, v_inv = codes ? 1.f / d.vs : 1.f;
-      bool fits = !values_odd<FMT>(w) && k_inv < INFINITY && v_inv < INFINITY;
+      bool fits = !words_odd<FMT>(w, p.two) && !values_odd<FMT>(w) && k_inv < INFINITY && v_inv < INFINITY;
       float amax_k = 0.f, amax_v = 0.f;
       for (int r = quant + (lane >> 4); r < kTile; r += 2) {
         float x[8], y[8];
@@ -334,8 +334,8 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
 // subtile ahead of the values, K(x) K(x + step) V(x) K(x + 2 step) V(x + step)
 // ..., so that a tile's last keys do not wait for the stage of its first
 // values, and packed words are on their way while others are turned into
-// halves.  Any other subtile is made on
-// its own between two runs, when no word is held.
+// halves.  Any other subtile, and one whose numbers may not fit a half, is
+// made on its own between two runs, when no word is held.
 template <int FMT, bool SHARED>
 __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, const UnitSrc<FMT>& unit, uint32_t k_tiles, uint32_t v_tiles, int pw, int step) {
   constexpr int kValueStages = value_stages(SHARED);
@@ -371,50 +371,53 @@ __device__ __forceinline__ void produce(const ChunkAttnArgs& A, ChunkCtrl& C, co
   int x = pw;
   while (x < last) {
     SubSrc d;
-    if (!packed(x, d)) {
-      // The softmax reads the description when the scores are there, so it has
-      // to be complete before the keys are handed over: rows that need a look
-      // give their values first.
-      if (!wait_keys(x) || !wait_values(x)) return;
-      const int g = x / kSubs, sub = x % kSubs;
-      const int kind = produce_other<FMT>(A, C, unit, tile(x) * kKeys + kTile * sub, key_tile(x), value_tile(x),
-                                          sub, C.info[g % kInfos]);
-      if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
-      hand_over(&C.k_full[g % kStages]);
-      hand_over(&C.v_full[g % kValueStages]);
-      x += step;
-      continue;
-    }
-    SubWords<FMT> w;
-    load_keys<FMT>(d, w);
-    bool more, two = false;                  // two: the held values have 2-bit codes
-    for (int y = -1;; y = x, x += step) {
-      // keys of x
-      const int g = x / kSubs;
-      if (!wait_keys(x)) return;
-      const bool two_here = d.two;
-      if (FMT == 6 && two_here) keys_to_tile<FMT, 2>(w, key_tile(x), x % kSubs);
-      else keys_to_tile<FMT, SubWords<FMT>::kBits>(w, key_tile(x), x % kSubs);
-      if (lane == 0) C.info[g % kInfos].kind[x % kSubs] = 0;
-      hand_over(&C.k_full[g % kStages]);
-      const SubSrc here = d;
-      more = x + step < last && packed(x + step, d);
-      if (more) load_keys<FMT>(d, w);
-      // values of y, the subtile before
+    if (packed(x, d)) {
+      SubWords<FMT> w;
+      load_keys<FMT>(d, w);
+      bool more = true, two = false;         // two: the held values have 2-bit codes
+      int y = -1;                            // whose values are held
+      while (more && !words_odd<FMT>(w, d.two)) {
+        // keys of x
+        const int g = x / kSubs;
+        if (!wait_keys(x)) return;
+        const bool two_here = d.two;
+        if (FMT == 6 && two_here) keys_to_tile<FMT, 2>(w, key_tile(x), x % kSubs);
+        else keys_to_tile<FMT, SubWords<FMT>::kBits>(w, key_tile(x), x % kSubs);
+        if (lane == 0) C.info[g % kInfos].kind[x % kSubs] = 0;
+        hand_over(&C.k_full[g % kStages]);
+        const SubSrc here = d;
+        more = x + step < last && packed(x + step, d);
+        if (more) load_keys<FMT>(d, w);
+        // values of y, the subtile before
+        if (y >= 0) {
+          if (!wait_values(y)) return;
+          if (FMT == 6 && two) values_to_tile<FMT, 2>(w, value_tile(y), y % kSubs);
+          else values_to_tile<FMT, SubWords<FMT>::kBits>(w, value_tile(y), y % kSubs);
+          hand_over(&C.v_full[(y / kSubs) % kValueStages]);
+        }
+        load_values<FMT>(here, w);
+        two = two_here;
+        y = x;
+        x += step;
+      }
       if (y >= 0) {
         if (!wait_values(y)) return;
         if (FMT == 6 && two) values_to_tile<FMT, 2>(w, value_tile(y), y % kSubs);
         else values_to_tile<FMT, SubWords<FMT>::kBits>(w, value_tile(y), y % kSubs);
         hand_over(&C.v_full[(y / kSubs) % kValueStages]);
       }
-      load_values<FMT>(here, w);
-      two = two_here;
-      if (!more) break;
+      if (!more) continue;                   // the next subtile is not a packed one
     }
-    if (!wait_values(x)) return;
-    if (FMT == 6 && two) values_to_tile<FMT, 2>(w, value_tile(x), x % kSubs);
-    else values_to_tile<FMT, SubWords<FMT>::kBits>(w, value_tile(x), x % kSubs);
-    hand_over(&C.v_full[(x / kSubs) % kValueStages]);
+    // The softmax reads the description when the scores are there, so it has
+    // to be complete before the keys are handed over: rows that need a look
+    // give their values first.
+    if (!wait_keys(x) || !wait_values(x)) return;
+    const int g = x / kSubs, sub = x % kSubs;
+    const int kind = produce_other<FMT>(A, C, unit, tile(x) * kKeys + kTile * sub, key_tile(x), value_tile(x), sub,
+                                        C.info[g % kInfos]);
+    if (lane == 0) C.info[g % kInfos].kind[sub] = (uint8_t)kind;
+    hand_over(&C.k_full[g % kStages]);
+    hand_over(&C.v_full[g % kValueStages]);
     x += step;
   }
 }
