@@ -44,7 +44,17 @@ constexpr int kStages = 2;                   // key tiles in flight
 __host__ __device__ constexpr int value_stages(bool shared_keys) { return shared_keys ? 2 : 3; }
 constexpr int kMaxValueStages = 3;
 constexpr int kInfos = 4;                    // tile descriptions in flight
-constexpr float kSlack = 14.f;               // the reference maximum may lag by 2^14 (P stays below fp16's 65504)
+// A row's reference is its maximum at first, and stays while no weight passes
+// 2^kTop (fp16 ends at 65504).  From the stream's half tile kSettle on, when
+// the maximum has mostly been seen, it lies 2^kLift lower: fp16 loses what is
+// below 2^-25, then 2^-31 of the largest weight; 131072 such tokens are 2^-14
+// of a row, where they would be 2^-8.  The price is one more scaling of O, and
+// a maximum that grows by 2^(kTop - kLift) moves the reference again: 2048
+// tokens over 32768 take 1307 us, 1295 without a lift, 1316 with one of 8; lifted
+// from the start, 2 x 1024 tokens in a window of 4096 + 4 (its first tile shows
+// four keys) take 600, 520 so.
+constexpr float kLift = 6.f, kTop = 15.f;
+constexpr int kSettle = 6;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // Eight channels of a query row (16 lanes a row) whose magnitudes need a power
@@ -517,14 +527,15 @@ struct Row {
   uint32_t ts, to;                           // TMEM addresses of the warp's scores and output
 };
 
-// Raises the row's reference to cover `top`, and O with it if it has to move;
+// Moves the row's reference to cover `top` if it has to, and O with it;
 // `turn` is the number of the half tile in the stream.  False: a wait was
 // given up.
 __device__ __forceinline__ bool raise(ChunkCtrl& C, int i, int turn, float top, Row& w) {
   RowState& r = w.r;
-  const bool up = top > r.m + kSlack || (r.m == -INFINITY && top > -INFINITY);
+  const bool settle = turn == kSettle && r.m > -INFINITY;
+  const bool up = settle || top > r.m + kTop || (r.m == -INFINITY && top > -INFINITY);
   if (!__any_sync(0xffffffffu, up)) return true;
-  const float mn = up ? top : r.m;
+  const float mn = up ? (settle ? fmaxf(top, r.m) : top) - (turn < kSettle ? 0.f : kLift) : r.m;
   const float f = r.m == -INFINITY ? (up ? 0.f : 1.f) : (up ? ex2(r.m - mn) : 1.f);
   if (turn > 0 && __any_sync(0xffffffffu, up && r.m != -INFINITY)) {
     // O is at rest once the P V of the half before this is done (the one

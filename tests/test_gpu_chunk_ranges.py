@@ -3,8 +3,11 @@ import numpy as np
 import pytest
 import torch
 
-from chunk_ref import bf16
-from test_gpu_chunk import FORMATS, Case, bits_of
+from bit_kv_cache_16_b200 import kvq
+from chunk_ref import attend, bf16, cached_rows
+from gpu_harness import to_dev
+from layout import GpuState
+from test_gpu_chunk import FORMATS, SCALE, Case, bits_of, cu_of
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +75,38 @@ def test_one_far_token_among_ordinary_ones(fmt, G, far):
     case.fill()
     case.check(case.attend())
     case.check(case.attend(splits=3, window=700, sinks=20), 700, 20)
+
+
+@pytest.mark.parametrize("fmt", [4, 8, 16])
+@pytest.mark.parametrize("sink_at", [0, 20000])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_many_small_weights_beside_a_sink(fmt, sink_at, splits):
+    """One token's logit about 17.7 above 40000 others whose weights, 2^-25.5 of the sink's each, are the whole output (the
+    sink's value is zero)."""
+    n, m = 40000, 3
+    rng = np.random.default_rng(fmt)
+    k = np.full((n, 2, 128), 0.609375)
+    k[sink_at] = 1.0
+    v = rng.uniform(0.5, 1.5, (n, 2, 128))
+    v[sink_at] = 0.0
+    c = kvq.Cache(fmt, 1, 8, 2, 40064, 32, 0)
+    if fmt == 8:
+        c.region("fp8_scale").view(torch.float32).copy_(torch.tensor([1.0 / 64, 1.0 / 64, 1.5 / 448, 1.5 / 448]))
+    c.append_chunk(to_dev(bits_of(k)), to_dev(bits_of(v)), cu_of([n]), n)
+    q = bits_of(np.full((m, 8, 128), 4.0))
+    kn, vn = bits_of(np.full((m, 2, 128), 0.609375)), bits_of(rng.uniform(0.5, 1.5, (m, 2, 128)))
+    out = torch.zeros(m, 8, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(c.chunk_workspace_bytes(splits, m, m, n), 16), dtype=torch.uint8, device="cuda")
+    c.chunk_attention(to_dev(q), to_dev(kn), to_dev(vn), cu_of([m]), m, out, SCALE, ws, splits, n)
+    for h in range(8):
+        kk, vv = cached_rows(GpuState(c), 0, h // 4)
+        kk, vv = np.concatenate([kk, bf16(kn[:, h // 4])]), np.concatenate([vv, bf16(vn[:, h // 4])])
+        ref, _, tol = attend(bf16(q[:, h]), kk, vv, np.arange(n, n + m), SCALE)
+        # attend allows each weight an error of 2^-25 of the largest.  Here that holds for a key range's first three tiles
+        # of 128 tokens; then weights are held at 2^6 times that and more, so that half a step of fp16's smallest numbers is
+        # 2^-31.  (Most of what is left of attend's tolerance is e^(2d) - 1 with d = 45.3 2^-11: keys rounded to halves.)
+        tol -= (2.0 ** -25 * (kk.shape[0] - 384) - 2.0 ** -31 * kk.shape[0]) * np.abs(vv).max()
+        # together 5.3 %, 2.0 % and 3.3 % of the output, where all the small weights were lost with the largest at 1
+        assert np.all(ref > 5e-4) and np.all(tol < 0.2 * ref)
+        assert np.all(np.abs(out[:, h].float().cpu().numpy() - ref) <= tol), h
+    assert c.error() == 0
