@@ -7,8 +7,8 @@
 // online softmax with one thread per row (64 keys at a time), P = fp16 back
 // into TMEM, O += P V with O in TMEM.  Packed tokens become fp16 operands once
 // per CTA and tile (kvq_tiles.cuh); fp16 holds every code exactly and a
-// dequantized number to 2^-11, eight times finer than bf16, and powers of two
-// are taken out of raw rows that would not fit.
+// dequantized number to 2^-11, eight times finer than bf16, and a power of two
+// is taken out of 16-token pieces whose numbers would not fit.
 //
 // What bounds it: a stream's tile is a chain (scores, maximum, weights, P V,
 // next scores) of about 2400 cycles of softmax and 1500 of products, and TMEM

@@ -72,8 +72,10 @@ __device__ __forceinline__ void put_value8(uint32_t tile, int r, int p, const fl
   st_shared16(piece_at(tile, r, p), pack_h2(x[0], x[1]), pack_h2(x[2], x[3]), pack_h2(x[4], x[5]), pack_h2(x[6], x[7]));
 }
 
-// Largest finite magnitude of rows -> the power e they are divided by (2^e):
-// 0 unless fp16 would overflow or lose bits of the largest numbers.
+// Largest finite magnitude of a subtile's rows -> the power e they are divided
+// by (2^e): 0 unless fp16 would overflow or lose bits of the largest numbers,
+// which otherwise come to [2^8, 2^9).  A bf16 number of 2^(e - 17) or more is
+// then a half as it is; smaller ones are off by 2^(e - 25) at most.
 __device__ __forceinline__ int tile_exponent(float amax) {
   if (amax == 0.f || (amax >= 0x1p-6f && amax < 0x1p15f)) return 0;
   return max((int)(__float_as_uint(amax) >> 23) - 127 - 8, -100);

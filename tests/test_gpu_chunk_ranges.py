@@ -110,3 +110,27 @@ def test_many_small_weights_beside_a_sink(fmt, sink_at, splits):
         assert np.all(ref > 5e-4) and np.all(tol < 0.2 * ref)
         assert np.all(np.abs(out[:, h].float().cpu().numpy() - ref) <= tol), h
     assert c.error() == 0
+
+
+@pytest.mark.parametrize("fmt", [4, 16])
+@pytest.mark.parametrize("top", [0, 14, 30, -20])
+@pytest.mark.parametrize("far", [12, 18, 22, 30])
+def test_tiny_new_token_beside_ordinary_ones(fmt, top, far):
+    """Sixteen new tokens share a piece; the first one's values lie 2^far below the others'.  Row 0 sees it alone: its output
+    is off by half a step of the smallest half in the piece's scale, and by the output's own rounding."""
+    case = Case(fmt, [0], [16], R=0, seed=250 + far)
+    rng = np.random.default_rng(far)
+    v = rng.uniform(0.5, 1.0, case.vn.shape) * 2.0 ** top
+    v[0] *= 2.0 ** -far
+    case.vn = bits_of(v)
+    out = case.attend()
+    case.check(out)
+    tiny = bf16(case.vn[0]).repeat(4, 0)                      # (8 query heads, 2 kv heads)
+    # nothing is taken out of a piece whose largest magnitude is in [2^-6, 2^15); otherwise that comes to [2^8, 2^9)
+    largest = np.abs(bf16(case.vn)).max((0, 2)).repeat(4)
+    e = np.where((largest >= 2.0 ** -6) & (largest < 2.0 ** 15), 0.0, np.floor(np.log2(largest)) - 8)
+    step = 2.0 ** (e - 25)[:, None]
+    assert np.all(np.abs(out[0] - tiny) <= step + 2.0 ** -8 * tiny)
+    # numbers down to 2^-17 in that scale are halves as they are
+    whole = tiny >= 2.0 ** (e - 17)[:, None]
+    assert np.all(out[0][whole] == tiny[whole])
