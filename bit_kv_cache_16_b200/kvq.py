@@ -414,9 +414,16 @@ class Cache:
         with torch.cuda.device(self._index):
             return fn(self.desc, *args, stream)
 
-    def reset(self):
+    def reset(self, stream=None):
         """Empty the cache: every sequence has no token (the FP8 scales stay)."""
-        self._counters.zero_()
+        if stream is None:
+            self._counters.zero_()
+            return
+        handle = _stream(stream).value or 0
+        # (no ExternalStream for the default stream's handle: torch takes 0 for "none given")
+        s = torch.cuda.ExternalStream(handle, self._index) if handle else torch.cuda.default_stream(self._index)
+        with torch.cuda.stream(s):
+            self._counters.zero_()
 
     def append_chunk(self, k_new, v_new, cu_seqlens, max_new: int, token_class=None, stream=None):
         """Append a ragged chunk: k_new, v_new bf16 [T, H_kv, 128], cu_seqlens int32 [B + 1]; token_class uint8 [T] for a

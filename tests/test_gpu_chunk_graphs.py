@@ -77,3 +77,26 @@ def test_replays_equal_calls(fmt, splits):
         case.check(one[0].float().cpu().numpy().astype(np.float64), 200, 4)
         put_back(c, after)
     assert c.error() == 0
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle", "default"])
+def test_reset_on_a_stream(kind):
+    """reset() given a stream takes its turn there: behind an append that waits, before the next one."""
+    case = Case(4, [50, 9], [20, 4], seed=320)
+    side = torch.cuda.default_stream() if kind == "default" else torch.cuda.Stream()
+    other = torch.cuda.Stream()
+    stream = side if kind == "stream" else side.cuda_stream
+    k, v, kn, vn = (to_dev(a) for a in (case.k, case.v, case.kn, case.vn))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):                            # the current stream is not the one that is given
+        for _ in range(3):
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20000000)                   # about 10 ms: a clear that did not wait would be long past
+            case.cache.append_chunk(k, v, case.cu, 50, stream=stream)
+            case.cache.reset(stream=stream)
+            case.cache.append_chunk(kn, vn, case.cu_new, 20, stream=stream)
+            torch.cuda.synchronize()
+            assert case.cache.seq_len()[:2].tolist() == [20, 4]
+            case.cache.reset(stream=stream)
+    torch.cuda.synchronize()
+    assert case.cache.seq_len()[:2].tolist() == [0, 0] and case.cache.error() == 0
