@@ -621,7 +621,7 @@ __device__ __forceinline__ void hide(float (&x)[32], uint32_t seen) {
 // registers, and the second half's are on their way while the first is weighed.
 __device__ __forceinline__ bool soft_plain(const ChunkAttnArgs& A, ChunkCtrl& C, int i, int it, bool all, int t0,
                                            int first_row, const Scaling& sc, Row& w) {
-  const float k = w.cm * sc.kmul;
+  const float k = fmaxf(w.cm * sc.kmul, 0x1p-126f);           // (not 0: hidden scores are -inf, and stay it)
   const pair_t k2 = pair(k, k);
   float xa[32], xb[32];
   tc_ld32(xa, w.ts);

@@ -134,3 +134,18 @@ def test_tiny_new_token_beside_ordinary_ones(fmt, top, far):
     # numbers down to 2^-17 in that scale are halves as they are
     whole = tiny >= 2.0 ** (e - 17)[:, None]
     assert np.all(out[0][whole] == tiny[whole])
+
+
+@pytest.mark.parametrize("qexp,scale_exp", [(-60, -30), (-110, -60), (-120, -90)])
+def test_scores_too_small_for_floats(qexp, scale_exp):
+    """Queries and FP8 key scales whose product is below every float: each visible token weighs the same."""
+    case = Case(8, [70, 300], [40, 9], seed=270)
+    s = case.cache.region("fp8_scale").view(torch.float32)
+    s[:2] = 2.0 ** scale_exp
+    case.k = bits_of(bf16(case.k) * 2.0 ** (scale_exp + 4))
+    case.kn = bits_of(bf16(case.kn) * 2.0 ** (scale_exp + 4))
+    case.q = bits_of(bf16(case.q) * 2.0 ** qexp)
+    case.fill()
+    case.check(case.attend())
+    case.check(case.attend(window=50, sinks=4), 50, 4)
+    assert case.cache.error() == 0
