@@ -275,8 +275,12 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       if (quant < kTile) drop_values<FMT>(w, quant);         // (what lies behind the end is not data)
       // raw rows take the codes' scaling (FP8), so that the subtile has one
       const float k_inv = codes ? 1.f / d.ks : 1.f, v_inv = codes ? 1.f / d.vs : 1.f;
-      bool fits = !words_odd<FMT>(w, p.two) && !values_odd<FMT>(w) && k_inv < INFINITY && v_inv < INFINITY;
+      bool fits = !__any_sync(0xffffffffu, keys_past<FMT>(w, p.two) != 0u) && !values_odd<FMT>(w) && k_inv < INFINITY && v_inv < INFINITY;
       float amax_k = 0.f, amax_v = 0.f;
+      if constexpr (FMT != 8) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) amax_v = fmaxf(amax_v, most_of<FMT>(w.vm[q], p.two));
+      }
       for (int r = quant + (lane >> 4); r < kTile; r += 2) {
         float x[8], y[8];
         unpack8(raw.load(base + r, r, lane & 15), x);
@@ -290,7 +294,15 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
       }
       amax_k = warp_max(amax_k);                             // (whole-warp shuffles: not behind a lane's own `fits`)
       amax_v = warp_max(amax_v);
-      fits = fits && tile_exponent(amax_k) == 0 && tile_exponent(amax_v) == 0;
+      fits = fits && tile_exponent(amax_k) == 0;
+      if (FMT == 8) {
+        fits = fits && (amax_v == 0.f || value_exponent(amax_v) == 0);      // (codes have the head's scale)
+      } else if (quant < kTile) {
+        fits = fits && value_exponent(amax_v) == 0;
+      } else if (amax_v < kLeastValue) {                     // small packed values: 2^ev out of their scales and zeros
+        ev = amax_v == 0.f ? kLeastPower : max(value_exponent(amax_v), -15);
+        if (amax_v > 0.f) scale_values<FMT>(w, -ev);
+      }
       if (__all_sync(0xffffffffu, fits)) {
         if (FMT == 6 && p.two) {
           keys_to_tile<FMT, 2>(w, kt, sub);
@@ -312,16 +324,25 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
           put_key8(kt, kTile * sub + row_of_token(r), lane & 15, x);
           put_value8(vt, kTile * sub + row_of_token(r), lane & 15, y);
         }
-        return 0;
+        if (ev == 0) return 0;
+        if (lane == 0) {
+          info.kmul[sub] = 1.f;
+          info.vlog[sub] = (float)ev;
+          info.vinv[sub] = scale_by(1.f, -ev);
+          info.bad[sub] = 0u;
+        }
+        return 2;
       }
+      ev = 0;
     }
     bool k_done = false, v_done = false;
     if (quant == 0 && !rope) {
       RawWords x[2];                                         // both on their way at once
       load_rows(raw, base, x[0]);
       load_rows(raw_v, base, x[1]);
-      k_done = rows_to_tile(x[0], kt, sub, true);
-      v_done = rows_to_tile(x[1], vt, sub, false);
+      const bool gone = base >= sq.total;
+      k_done = rows_to_tile(x[0], kt, sub, true, gone);
+      v_done = rows_to_tile(x[1], vt, sub, false, gone);
     }
     if (codes && quant == kTile) d.ks = d.vs = 1.f;          // (with raw rows: in natural scale, kind 1)
     if (!k_done) ek = keys_any<FMT>(d, quant, raw, base, rope ? C.freq : nullptr, kt, sub);

@@ -80,6 +80,21 @@ __device__ __forceinline__ int tile_exponent(float amax) {
   if (amax == 0.f || (amax >= 0x1p-6f && amax < 0x1p15f)) return 0;
   return max((int)(__float_as_uint(amax) >> 23) - 127 - 8, -100);
 }
+// The same for values, whose power is a factor of the softmax weights too: P
+// carries 2^e, so pieces of one row should not differ in e for no reason.
+// Nothing is taken out of [2^-8, 2^15); smaller ones come to [2^-2, 2^-1), only
+// so far up that a half holds them, larger ones to [2^8, 2^9); zeros hold back
+// nobody's weights.  (With packed pieces always at e = 0 and small raw ones
+// brought to 2^8, an INT cache whose values were all about 2^-13 gave its new
+// tokens' weights 2^-21 of their size, in halves.)
+constexpr int kLeastPower = -90;
+constexpr float kLeastValue = 0x1p-8f;
+__device__ __forceinline__ int value_exponent(float amax) {
+  if (amax == 0.f) return kLeastPower;
+  if (amax >= kLeastValue && amax < 0x1p15f) return 0;
+  const int lg = (int)(__float_as_uint(amax) >> 23) - 127;
+  return lg > 0 ? lg - 8 : max(lg + 2, kLeastPower);
+}
 // x * 2^e for |e| <= 252, in two steps so that neither factor overflows.
 __device__ __forceinline__ float scale_by(float x, int e) {
   const int a = e / 2, b = e - a;
@@ -404,6 +419,8 @@ __device__ __forceinline__ uint32_t larger_half(uint32_t m) { return max(m & 0xF
 
 // A largest bf16 magnitude that fp16 takes as it is: 0, or in [2^-6, 2^15).
 __device__ __forceinline__ bool ordinary(uint32_t m) { return m == 0u || (m >= 0x3C80u && m < 0x4700u); }
+// The same for values: in [2^-8, 2^15).
+__device__ __forceinline__ bool ordinary_value(uint32_t m) { return m >= 0x3B80u && m < 0x4700u; }
 
 // Eight bf16 numbers -> four fp16 pairs, in the key tiles' channel order or in order.
 __device__ __forceinline__ void put_raw8(uint32_t at, const uint4& w, bool key) {
@@ -415,7 +432,7 @@ __device__ __forceinline__ void put_raw8(uint32_t at, const uint4& w, bool key) 
 
 // Sixteen bf16 rows, as loaded (piece lane % 16 of rows 2i + lane / 16), into a
 // tile.  False, and nothing written, if a number is not finite or the
-// magnitudes need a power of two taken out.
+// magnitudes need a power of two taken out.  gone: none of the rows is a token.
 struct RawWords {
   uint4 w[8];
 };
@@ -424,13 +441,13 @@ __device__ __forceinline__ void load_rows(const RawRows& raw, int base, RawWords
 #pragma unroll
   for (int i = 0; i < 8; ++i) x.w[i] = raw.load(base + 2 * i + half, 2 * i + half, p);
 }
-__device__ __forceinline__ bool rows_to_tile(const RawWords& x, uint32_t tile, int sub, bool key) {
+__device__ __forceinline__ bool rows_to_tile(const RawWords& x, uint32_t tile, int sub, bool key, bool gone) {
   const int lane = threadIdx.x & 31, p = lane & 15, half = lane >> 4;
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = abs_max8(m, x.w[i]);
   m = __reduce_max_sync(0xffffffffu, larger_half(m));
-  if (!ordinary(m)) return false;
+  if (!(key ? ordinary(m) : ordinary_value(m) || (gone && m == 0u))) return false;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     put_raw8(piece_at(tile, kTile * sub + 4 * (i >> 1) + 2 * half + (i & 1), p), x.w[i], key);
@@ -479,40 +496,71 @@ __device__ __forceinline__ bool values_odd(const SubWords<FMT>& w) {
   return __any_sync(0xffffffffu, odd != 0u);
 }
 
-// Whether a key or value of the subtile could be anything but a finite half,
-// from the words that load_keys has: code * scale + zero is taken in halves on
-// the way to the tiles, and may pass 65504 where scale and zero do not (minimum
-// 0 and maximum 100000 make an INT4 scale of 6668).  Such a subtile goes
-// through keys_any / values_any.  Integer maxima, since infinities and NaN are
-// the largest patterns.  FP8 codes are halves as they are.  Cost: 766 against
-// 760 us for 2048 tokens over 16384 INT4 ones, 862 against 836 for MIXED.
+// The most that code * scale + zero can be in magnitude (infinities and NaN
+// come out on top as bit patterns, sign aside).
+template <int FMT>
+__device__ __forceinline__ float most_of(uint32_t m, bool two) {
+  const float top = FMT == 16 ? 255.f : FMT == 2 || (FMT == 6 && two) ? 3.f : 15.f;
+  return fmaf(top, __low2float(u32_as_h2(m)), fabsf(__high2float(u32_as_h2(m))));
+}
+
+// The scales and zeros of the lane's values times 2^e, 0 <= e <= 15 (exact).
+template <int FMT>
+__device__ __forceinline__ void scale_values(SubWords<FMT>& w, int e) {
+  const uint32_t f = (uint32_t)(15 + e) << 10;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) asm("mul.rn.f16x2 %0, %0, %1;\n" : "+r"(w.vm[q]) : "r"(f | (f << 16)));
+}
+
+// Non-zero if a key of the lane could be anything but a finite half: code *
+// scale + zero is taken in halves on the way to the tiles, and may pass 65504
+// where scale and zero do not (minimum 0 and maximum 100000 make an INT4 scale
+// of 6668).  FP8 codes are halves as they are.
+template <int FMT>
+__device__ __forceinline__ uint32_t keys_past(const SubWords<FMT>& w, bool two) {
+  uint32_t odd = 0u;
+  if constexpr (FMT == 16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd |= past_half<FMT>(w.km[i]);
+  } else if constexpr (FMT != 8) {
+    auto larger = [](uint32_t a, uint32_t b) {               // of the magnitudes; NaN stays
+      return h2_as_u32(__hmax2_nan(__habs2(u32_as_h2(a)), __habs2(u32_as_h2(b))));
+    };
+    uint32_t sc, ze;
+    if (FMT == 2 || (FMT == 6 && two)) {
+      constexpr int z = SubWords<FMT>::kKM / 2;
+      sc = larger(larger(larger(w.km[0], w.km[1]), larger(w.km[2], w.km[3])),
+                  larger(larger(w.km[4], w.km[5]), larger(w.km[6], w.km[7])));
+      ze = larger(larger(larger(w.km[z], w.km[z + 1]), larger(w.km[z + 2], w.km[z + 3])),
+                  larger(larger(w.km[z + 4], w.km[z + 5]), larger(w.km[z + 6], w.km[z + 7])));
+    } else {
+      sc = larger(larger(w.km[0], w.km[1]), larger(w.km[2], w.km[3]));
+      ze = larger(larger(w.km[4], w.km[5]), larger(w.km[6], w.km[7]));
+    }
+    odd |= past_half<FMT>(prmt(sc, ze, 0x5410u)) | past_half<FMT>(prmt(sc, ze, 0x7632u));
+  }
+  return odd;
+}
+
+// Non-zero unless code * scale + zero stays below kLeastValue: |zero| < 2^-9 and
+// scale < 2^-13 (INT2: 2^-11, INT8: 2^-17).
+template <int FMT>
+__device__ __forceinline__ uint32_t not_small(uint32_t m) {
+  constexpr uint32_t least = FMT == 16 ? 0x0080u : FMT == 2 ? 0x1000u : 0x0800u;
+  return ((m & 0x7FFF7FFFu) + (((0x8000u - 0x1800u) << 16) | (0x8000u - least))) & 0x80008000u;
+}
+
+// Whether a subtile needs a closer look, from the words that load_keys has: a
+// key or value may not be a finite half, or all values are small, and a power
+// of two is taken out.  Cost: 1 % of 2048 tokens over 16384 (760 us), 3 % of
+// MIXED, whose producers are the bound (836 us).
 template <int FMT>
 __device__ __forceinline__ bool words_odd(const SubWords<FMT>& w, bool two) {
   if constexpr (FMT == 8) {
     return false;
   } else {
-    uint32_t odd = past_half<FMT>(w.probe);
-    if constexpr (FMT == 16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) odd |= past_half<FMT>(w.km[i]);
-    } else {
-      uint32_t sc = 0u, ze = 0u;
-      if (FMT == 2 || (FMT == 6 && two)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sc = __vmaxu2(sc, w.km[i]);
-          ze = abs_max2(ze, w.km[SubWords<FMT>::kKM / 2 + i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc = __vmaxu2(sc, w.km[i]);
-          ze = abs_max2(ze, w.km[4 + i]);
-        }
-      }
-      odd |= past_half<FMT>(prmt(sc, ze, 0x5410u)) | past_half<FMT>(prmt(sc, ze, 0x7632u));
-    }
-    return __any_sync(0xffffffffu, odd != 0u);
+    return __any_sync(0xffffffffu, (keys_past<FMT>(w, two) | past_half<FMT>(w.probe)) != 0u) ||
+           !__any_sync(0xffffffffu, not_small<FMT>(w.probe) != 0u);
   }
 }
 
@@ -610,7 +658,7 @@ __device__ __noinline__ int values_any(const TileSrc& d, int quant, const RawRow
       one(r, 8 * p, x);
     }
     if (pass == 0) {
-      e = tile_exponent(warp_max(amax));
+      e = value_exponent(warp_max(amax));
       mine = __reduce_or_sync(0xffffffffu, mine);
     }
   }

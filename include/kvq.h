@@ -470,8 +470,9 @@ kvq_status kvq_read_tokens(const kvq_cache *cache, const int32_t *start_dev, con
  * Precision: keys, values and softmax weights enter the products as halves,
  * sums are fp32, the output is rounded once.  Numbers are right to 2^-11, or to
  * 2^-25 in the scale of their 16 tokens: a power of two is taken out where the
- * largest magnitude of these is outside [2^-6, 2^15).  A row that sees a value
- * that is not finite is NaN; one that does not is not touched by it.
+ * largest magnitude of these is outside [2^-6, 2^15) (values: [2^-8, 2^15)).
+ * A row that sees a value that is not finite is NaN; one that does not is not
+ * touched by it.
  * A sequence with an inconsistent state (KVQ_DEVERR_STATE) or a chunk longer
  * than max_new or outside [0, total_new) (KVQ_DEVERR_PREFILL_LEN) is skipped,
  * its rows left as they were; the tokens of a page whose id is out of range

@@ -126,9 +126,11 @@ def test_tiny_new_token_beside_ordinary_ones(fmt, top, far):
     out = case.attend()
     case.check(out)
     tiny = bf16(case.vn[0]).repeat(4, 0)                      # (8 query heads, 2 kv heads)
-    # nothing is taken out of a piece whose largest magnitude is in [2^-6, 2^15); otherwise that comes to [2^8, 2^9)
+    # nothing is taken out of a piece whose largest magnitude is in [2^-8, 2^15); otherwise that comes to [2^-2, 2^-1) or
+    # [2^8, 2^9)
     largest = np.abs(bf16(case.vn)).max((0, 2)).repeat(4)
-    e = np.where((largest >= 2.0 ** -6) & (largest < 2.0 ** 15), 0.0, np.floor(np.log2(largest)) - 8)
+    e = np.floor(np.log2(largest))
+    e = np.where((largest >= 2.0 ** -8) & (largest < 2.0 ** 15), 0.0, np.where(largest < 1, e + 2, e - 8))
     step = 2.0 ** (e - 25)[:, None]
     assert np.all(np.abs(out[0] - tiny) <= step + 2.0 ** -8 * tiny)
     # numbers down to 2^-17 in that scale are halves as they are
@@ -148,4 +150,61 @@ def test_scores_too_small_for_floats(qexp, scale_exp):
     case.fill()
     case.check(case.attend())
     case.check(case.attend(window=50, sinks=4), 50, 4)
+    assert case.cache.error() == 0
+
+
+
+@pytest.mark.parametrize("fmt,G,R,paged", FORMATS)
+@pytest.mark.parametrize("vexp", [-6, -8, -10, -13, -16, -20, -30, -60])
+def test_small_values(fmt, G, R, paged, vexp):
+    """All values about 2^vexp: packed, window and new tokens in one key range, their weights held alike."""
+    case = Case(fmt, [200, 37, 70, 0], [40, 20, 9, 3], G=G, R=R, paged=paged, seed=260 + G)
+    case.v, case.vn = bits_of(bf16(case.v) * 2.0 ** vexp), bits_of(bf16(case.vn) * 2.0 ** vexp)
+    if fmt == 8:
+        s = case.cache.region("fp8_scale").view(torch.float32)
+        s[2:4] = s[2:4] * 2.0 ** vexp
+    case.fill()
+    check_small(case, case.attend(splits=1))
+    check_small(case, case.attend(splits=1, window=90, sinks=20), 90, 20)
+    assert case.cache.error() == 0
+
+
+def check_small(case, out, window=0, sinks=0):
+    """Case.check, with the tolerance for weights: halves of 2^-25 in units of the largest product of a weight and its piece's
+    power.  A value stands for 2^-e of itself, so the output is off by N 2^-25 |v| 2^d if the pieces' powers are within 2^d of
+    another: 2^4 (their largest values, a packed piece's taken as scale * top + zero), and 2^6 more about 2^-8, where none is
+    taken out any more.  Raw values are held to 2^-25 in that scale: 2^-17 of their piece's largest."""
+    st, at = GpuState(case.cache), 0
+    for b, (n, m) in enumerate(zip(case.lens, case.new)):
+        for h in range(8):
+            k, v = cached_rows(st, b, h // 4)
+            k = np.concatenate([k, bf16(case.kn[at:at + m, h // 4])])
+            v = np.concatenate([v, bf16(case.vn[at:at + m, h // 4])])
+            ref, _, tol = attend(bf16(case.q[at:at + m, h]), k, v, np.arange(n, n + m), SCALE, window, sinks)
+            largest = np.abs(v).max()
+            d = 10 if 2.0 ** -10 < largest < 2.0 ** -4 else 4
+            tol += largest * (k.shape[0] * (2.0 ** (d - 25) - 2.0 ** -25) + 2.0 ** -17) - 1e-30
+            err = np.abs(out[at:at + m, h] - ref)
+            assert np.all(err <= tol), (b, h, float(np.max(err / tol)))
+        at += m
+
+
+@pytest.mark.parametrize("fmt", [2, 4, 6, 8, 16])
+@pytest.mark.parametrize("zero", ["cached", "some cached", "new"])
+def test_zero_values_beside_small_ones(fmt, zero):
+    """Pieces whose values are all zero have weights but do not push those of small values out of the halves' range."""
+    case = Case(fmt, [200, 33], [40, 9], R=0, seed=265)
+    rng = np.random.default_rng(fmt)
+    small = lambda a: bits_of(rng.uniform(0.5, 1.0, a.shape) * 2.0 ** -15)
+    case.v, case.vn = small(case.v), small(case.vn)
+    if zero == "cached":
+        case.v[:] = 0
+    elif zero == "some cached":
+        case.v[:64] = 0
+    else:
+        case.vn[:] = 0
+    if fmt == 8:
+        case.cache.region("fp8_scale").view(torch.float32)[2:4] = 2.0 ** -15 / 448
+    case.fill()
+    check_small(case, case.attend(splits=1))
     assert case.cache.error() == 0
