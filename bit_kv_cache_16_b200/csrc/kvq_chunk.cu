@@ -223,9 +223,12 @@ __device__ __forceinline__ uint32_t tm_o(uint32_t tmem, int i) { return tmem + 2
 struct Scaling {
   float kmul, vlog, vinv;
 };
-// FP8 codes stand for themselves in the tiles; the head's static scales come in here.
+// FP8 codes stand for themselves in the tiles; the head's static scales come in
+// here.  (A value scale below kLeastScale, whose inverse times a row's weights
+// could pass fp32, does not: such a head's tokens go through values_any.)
+constexpr float kLeastScale = 0x1p-90f;
 __device__ __forceinline__ Scaling static_scaling(const kvq_cache& c, int kv) {
-  const float vs = fmaxf(c.fp8_scale[c.shape.num_kv_heads + kv], 0x1p-100f);
+  const float vs = fmaxf(c.fp8_scale[c.shape.num_kv_heads + kv], kLeastScale);
   return Scaling{c.fp8_scale[kv], log2f(vs), 1.f / vs};
 }
 
@@ -241,10 +244,11 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
   const bool rope = s.rope_theta > 0.f;
   const int lane = threadIdx.x & 31;
   const int quant = min(max(sq.nq - base, 0), kTile);        // quantized rows come first
-  const bool codes = FMT == 8 && quant > 0;                  // (codes as they are: the static scales come in later)
+  bool codes = FMT == 8 && quant > 0;                        // (codes as they are: the static scales come in later)
   int ek = 0, ev = 0;
   uint32_t bad = 0u;
   TileSrc d;
+  if constexpr (FMT == 8) d.vs = 1.f;
   if (quant > 0 && !tile_src<FMT>(c, C.work.b, C.work.kv, base / kTile, d)) {
     if (lane == 0) atomicOr(c.err_word, KVQ_DEVERR_PAGE_RANGE);
     zero_rows(kt, sub);
@@ -264,7 +268,9 @@ __device__ __noinline__ int produce_other(const ChunkAttnArgs& A, ChunkCtrl& C, 
     raw.fresh = A.k + at;
     raw_v.ring = (const uint16_t*)c.v_res + ring;
     raw_v.fresh = A.v + at;
-    if (quant > 0 && !rope && !s.sparse) {
+    bool packed = quant > 0 && !rope && !s.sparse;
+    if constexpr (FMT == 8) codes = packed = codes && d.vs >= kLeastScale;
+    if (packed) {
       // packed words: a tile at the window's edge, or (8-bit formats) the
       // sequence's last one with the chunk's first tokens behind it
       SubSrc p;
@@ -962,6 +968,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attention_kernel(const
     }
     fence_async();
   }
+  if (FMT == 8 && tid == 0 && A.c.fp8_scale[s.num_kv_heads + W.kv] < kLeastScale) C.straight = 0;
   tc_before();
   __syncthreads();
   tc_after();

@@ -75,10 +75,12 @@ __device__ __forceinline__ void put_value8(uint32_t tile, int r, int p, const fl
 // Largest finite magnitude of a subtile's rows -> the power e they are divided
 // by (2^e): 0 unless fp16 would overflow or lose bits of the largest numbers,
 // which otherwise come to [2^8, 2^9).  A bf16 number of 2^(e - 17) or more is
-// then a half as it is; smaller ones are off by 2^(e - 25) at most.
+// then a half as it is; smaller ones are off by 2^(e - 25) at most.  (No less
+// than 2^-90, whose inverse times a row's weights stays in fp32.)
+constexpr int kLeastPower = -90;
 __device__ __forceinline__ int tile_exponent(float amax) {
   if (amax == 0.f || (amax >= 0x1p-6f && amax < 0x1p15f)) return 0;
-  return max((int)(__float_as_uint(amax) >> 23) - 127 - 8, -100);
+  return max((int)(__float_as_uint(amax) >> 23) - 127 - 8, kLeastPower);
 }
 // The same for values, whose power is a factor of the softmax weights too: P
 // carries 2^e, so pieces of one row should not differ in e for no reason.
@@ -87,7 +89,6 @@ __device__ __forceinline__ int tile_exponent(float amax) {
 // nobody's weights.  (With packed pieces always at e = 0 and small raw ones
 // brought to 2^8, an INT cache whose values were all about 2^-13 gave its new
 // tokens' weights 2^-21 of their size, in halves.)
-constexpr int kLeastPower = -90;
 constexpr float kLeastValue = 0x1p-8f;
 __device__ __forceinline__ int value_exponent(float amax) {
   if (amax == 0.f) return kLeastPower;

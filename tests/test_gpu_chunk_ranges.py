@@ -208,3 +208,25 @@ def test_zero_values_beside_small_ones(fmt, zero):
     case.fill()
     check_small(case, case.attend(splits=1))
     assert case.cache.error() == 0
+
+
+@pytest.mark.parametrize("n", [70, 300])
+@pytest.mark.parametrize("cached,new", [(-95, -95), (-110, -110), (-110, -97), (-80, -110)])
+def test_values_too_small_for_a_scale(n, cached, new):
+    """FP8 value scales and new values near the smallest floats: right to what halves keep in a scale of 2^-90."""
+    case = Case(8, [n], [40], seed=280)
+    case.v, case.vn = bits_of(bf16(case.v) * 2.0 ** cached), bits_of(bf16(case.vn) * 2.0 ** new)
+    s = case.cache.region("fp8_scale").view(torch.float32)
+    s[2:4] = 2.0 ** (cached - 6)
+    case.fill()
+    for window, sinks in ((0, 0), (50, 4)):
+        out = case.attend(window=window, sinks=sinks)
+        # no power below 2^-90 is taken out, where half a step of the smallest halves is 2^-115
+        st = GpuState(case.cache)
+        for h in range(8):
+            k, v = cached_rows(st, 0, h // 4)
+            k, v = np.concatenate([k, bf16(case.kn[:, h // 4])]), np.concatenate([v, bf16(case.vn[:, h // 4])])
+            ref, _, tol = attend(bf16(case.q[:, h]), k, v, n + np.arange(40), SCALE, window, sinks)
+            tol += 2.0 ** -115 + k.shape[0] * 2.0 ** (4 - 25) * np.abs(v).max() - 1e-30      # (weights: check_small's)
+            assert np.all(np.abs(out[:, h] - ref) <= tol), (h, float(np.max(np.abs(out[:, h] - ref) / tol)))
+    assert case.cache.error() == 0
