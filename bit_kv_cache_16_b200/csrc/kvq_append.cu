@@ -75,8 +75,11 @@ __device__ __forceinline__ void ring_put(const kvq_cache& c, const uint16_t* k, 
 //  * the others: 32 new window tokens each whose slots held nothing.
 // seq_len, n_quant and the MIXED window classes are read by every CTA of the
 // sequence here and change in append_chunk_commit_kernel.
-// Bound by the encoder's instructions and the short waves of CTAs, not by
-// memory: 8 x 1048 INT4 tokens (8 heads) joining 1000 each take 22 us, 44 MB.
+// 8 x 1048 INT4 tokens (8 heads) joining 1000 each: 22 us, 44 MB (floor 6.7).
+// No limit of the machine is reached (issue slots 50 %, DRAM 23 %, 30 % of the
+// warps): a CTA loads, reduces, encodes and stores one group with nothing of
+// the next on its way, in 2.7 waves.  65536 tokens of one sequence: 75 us, 4.6
+// TB/s, 0.71 of the copy.
 // FMT: 2, 4 or 6 (MIXED).
 template <int FMT, int G, bool SPARSE>
 __global__ void __launch_bounds__(128, SPARSE ? 5 : (G <= 32 ? 6 : 5))

@@ -13,13 +13,14 @@
 // What bounds it: a stream's tile is a chain (scores, maximum, weights, P V,
 // next scores) of about 2400 cycles of softmax and 1500 of products, and TMEM
 // has room for two streams (S or P and O: 256 columns each).  Together a tile
-// of 256 rows takes about 4400 cycles, of which the tensor pipe is busy 45 %,
-// the exponential unit 45 %, the issue slots 48 %.  Measured alone with a cold
-// L2: 2048 tokens over 32768 INT4 tokens, 32 / 8 heads, 1275 us (889 TFLOP/s);
-// 1000 over 65536 INT2 tokens, 64 / 8 heads, 2108 us (1026); 2 x 1024 in a
+// of 256 rows takes about 4500 cycles, of which the tensor pipe is busy 44 %,
+// the exponential unit 44 %, the issue slots 48 %.  Measured alone with a cold
+// L2: 2048 tokens over 32768 INT4 tokens, 32 / 8 heads, 1306 us (868 TFLOP/s);
+// 1000 over 65536 INT2 tokens, 64 / 8 heads, 2175 us (995); 2 x 1024 in a
 // window of 4096 + 4 over FP8, 525 us (524; 480 with a warm L2); 6 tokens over
-// 8 x 8192 INT4, 68 us (1.2 TB/s of packed tokens: the paired form's chain of 33
-// tiles a CTA).
+// 8 x 8192 INT4, 70 us (1.2 TB/s of packed tokens: the paired form's chain of 33
+// tiles a CTA).  Keys before RoPE and dense-and-sparse caches (keys_any /
+// values_any for every piece): 2048 over 16384, 7160 and 6500 us, 785 without.
 //
 // Sixteen warps, because a seventeenth would leave 96 registers a thread, and
 // a spilled register is a trip to L2 here (shared memory takes the whole L1):
@@ -1043,8 +1044,8 @@ size_t chunk_workspace_bytes(const kvq_shape& s, int num_splits, int rows) {
 
 // Key ranges per row block: the fewest rounds of CTAs over the SMs, counting
 // what a CTA costs beside its tiles (set-up and output, worth about four
-// tiles).  2048 tokens over 32768 (256 row blocks): 1 range 1313 us, 4 1279;
-// 6 tokens over 8 x 8192: 1 range 101 us, 2 ranges 69.
+// tiles).  2048 tokens over 32768 (256 row blocks): 1 range 1317 us, 4 1316;
+// 6 tokens over 8 x 8192: 1 range 104 us, 2 ranges 69, 4 77.
 int chunk_default_splits(const kvq_shape& s, int rows, int max_new, int max_len, int window, int sinks) {
   const long long span = window > 0 ? min((long long)max_len + max_new, (long long)window + sinks + max_new)
                                     : (long long)max_len + max_new;

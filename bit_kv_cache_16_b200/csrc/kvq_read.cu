@@ -19,8 +19,8 @@ struct ReadArgs {
 // is a window) or held in the window ring.  Bound by the bf16 rows it writes:
 // the heads are neighbours in the grid, as their rows are in memory, and every
 // store of a value row is 32 bytes, a whole sector.  131072 INT2 tokens of 8
-// heads: 117 us, 5.4 TB/s (147 with a head's tiles side by side and 16-byte
-// stores); 16 x 4096 FP8 tokens: 74 us, 5.4 TB/s.  Several tile pairs per CTA
+// heads: 117 to 119 us, 5.3 TB/s (147 with a head's tiles side by side and
+// 16-byte stores); 16 x 4096 FP8 tokens: 77 us, 5.2 TB/s.  Several tile pairs per CTA
 // took 141 to 160 us, 8 CTAs per SM 139.
 template <int FMT>
 __global__ void __launch_bounds__(128, 16) read_tokens_kernel(ReadArgs A) {

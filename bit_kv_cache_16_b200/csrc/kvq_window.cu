@@ -3,9 +3,10 @@
 // hold visible tokens enter the list the warps stream; a chunk at an edge has
 // its hidden tokens' scores set to -inf and their scales, zeros and codes to
 // zero, so that nothing stored there (NaN and infinities too) reaches a sum.
-// 65000 + 128 of 131072 INT8 tokens, batch 2, 64 / 8 heads: 67 us, 4.1 TB/s,
+// 65000 + 128 of 131072 INT8 tokens, batch 2, 64 / 8 heads: 68 us, 4.1 TB/s,
 // bound as the full decode by each chunk's chain of conversions; 1024 + 4 of
-// 8192 INT4 tokens, batch 8, 32 / 8 heads: 16 us, the latency of two launches.
+// 8192 INT4 tokens, batch 8, 32 / 8 heads: 16 us, one or two chunks a warp and
+// so the fixed part of both kernels (alone under ncu 13 and 7 us).
 #include "kvq_decode.cuh"
 
 namespace kvq {
